@@ -1,0 +1,538 @@
+"""Measured cases of the 4-bit KV cache operators: append, read, attention and eviction.
+
+The cache is paged.  One page of one KV head holds P tokens of D channels as
+E2M1 values (4 bits) in blocks of 32 channels that share an E8M0 scale, in
+17/16 P D bytes (even channel in a byte's low nibble):
+
+    K codes   [P][D/2]              K scales  [P][D/32]
+    V codes   [P/4][16][4][D/32]    V scales  [P/4][D/32][4]
+
+in the order K codes, V codes, K scales, V scales.  A V byte's indexes are
+token / 4, channel / (D/16), token % 4 and the byte within the D/16 channels.
+
+``own`` false computes every operator with elementary torch operations in 32
+bits; true calls the package.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+if torch.cuda.is_available():
+    DEV = "cuda"
+else:
+    DEV = "cpu"
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "e5m2": torch.float8_e5m2}
+
+
+# --------------------------------------------------------------------- cases
+def listed():
+    return [
+        # one decoding step's new tokens of a batch go into the cache and are read back: the smallest call
+        {"name": "append_step", "op": "append", "seqs": 64, "longest": 4097, "new": 1, "kv": 8, "dim": 128,
+         "page": 16, "type": "bf16", "mix": 1},
+        # a packed batch of ragged prompts, K and V strided inside one projection's output, put away and read back
+        {"name": "append_prompt", "op": "append", "seqs": 5, "longest": 8192, "new": 0, "kv": 8, "dim": 128,
+         "page": 64, "type": "bf16", "mix": 2},
+        # the 8-bit cache of a long-context layer (4 KV heads) that arrived from the prefill side
+        {"name": "append_e5m2", "op": "append", "seqs": 2, "longest": 32768, "new": 0, "kv": 4, "dim": 128,
+         "page": 128, "type": "e5m2", "mix": 3},
+        # a sequence is handed to another node: its whole cache back as BF16
+        {"name": "read_handover", "op": "read", "seqs": 2, "longest": 16385, "new": 0, "kv": 8, "dim": 128,
+         "page": 64, "type": "bf16", "mix": 4},
+        # one user, one token: latency
+        {"name": "decode_one", "op": "attend", "seqs": 1, "longest": 777, "new": 1, "heads": 32, "kv": 8, "dim": 128,
+         "page": 16, "type": "bf16", "mass": False, "lse": False, "mix": 5},
+        # a serving batch in steady state, ragged, with the weights that the eviction uses
+        {"name": "decode_batch", "op": "attend", "seqs": 32, "longest": 8192, "new": 1, "heads": 32, "kv": 8,
+         "dim": 128, "page": 16, "type": "bf16", "mass": True, "lse": False, "mix": 6},
+        # long contexts, few sequences, groups of 8: the split over the long axis
+        {"name": "decode_long", "op": "attend", "seqs": 4, "longest": 131072, "new": 1, "heads": 64, "kv": 8,
+         "dim": 128, "page": 64, "type": "bf16", "mass": False, "lse": True, "mix": 7},
+        # five draft tokens a sequence checked at once, odd groups of 7, half precision, small heads
+        {"name": "draft_check", "op": "attend", "seqs": 24, "longest": 4095, "new": 5, "heads": 28, "kv": 4,
+         "dim": 64, "page": 32, "type": "fp16", "mass": True, "lse": False, "mix": 8},
+        # chunks of prompts behind ragged contexts, weights accumulated over the chunk's queries
+        {"name": "extend_chunk", "op": "attend", "seqs": 3, "longest": 16384, "new": 1021, "heads": 32, "kv": 8,
+         "dim": 128, "page": 64, "type": "bf16", "mass": True, "lse": True, "mix": 9},
+        # whole packed prompts
+        {"name": "prompt", "op": "attend", "seqs": 2, "longest": 8192, "new": 0, "heads": 32, "kv": 8, "dim": 128,
+         "page": 64, "type": "bf16", "mass": False, "lse": False, "mix": 10},
+        # one token over budget in every sequence of a batch: the eviction of each decoding step
+        {"name": "evict_step", "op": "evict", "seqs": 64, "longest": 2049, "budget": 2048, "sinks": 4, "recent": 64,
+         "kv": 8, "dim": 128, "page": 16, "even": True, "mix": 11},
+        # long contexts cut to an eighth after their prompts
+        {"name": "evict_long", "op": "evict", "seqs": 3, "longest": 131072, "budget": 16384, "sinks": 4,
+         "recent": 256, "kv": 8, "dim": 128, "page": 64, "even": False, "mix": 12},
+    ]
+
+
+def _spread(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.49)))))))
+
+
+def draw(rng):
+    op = rng.choice(["append", "read", "attend", "attend", "attend", "evict"])
+    c = {"op": op, "kv": rng.choice([1, 2, 3, 4, 8]), "dim": rng.choice([64, 128, 128, 256]),
+         "page": rng.choice([16, 32, 64, 128, 256]), "mix": rng.randrange(1 << 30)}
+    if op in ("append", "read"):
+        c["type"] = rng.choice(["bf16", "fp16", "e5m2"] if op == "append" else ["bf16", "fp16"])
+        c["seqs"] = _spread(rng, 1, 64)
+        c["longest"] = _spread(rng, 1, max(1, min(32768, 65536 * 4 * 128 // (c["seqs"] * c["kv"] * c["dim"]))))
+        c["new"] = rng.choice([0, 0, 1, _spread(rng, 1, c["longest"])])
+    elif op == "attend":
+        c["type"] = rng.choice(["bf16", "fp16"])
+        c["heads"] = c["kv"] * rng.choice([1, 2, 4, 5, 7, 8, 16])
+        c["new"] = rng.choice([1, 1, _spread(rng, 2, 12), _spread(rng, 13, 1500), 0])
+        c["seqs"] = _spread(rng, 1, 64) if 0 < c["new"] <= 12 else _spread(rng, 1, 4)
+        room = 4 * 131072 * 8 * 128 // (2 * c["seqs"] * c["kv"] * c["dim"])
+        rows = c["new"] * c["seqs"] * c["heads"] * c["dim"]
+        if c["new"] > 12:  # the listed prompts' pairs bound a chunk's
+            room = min(room, 32 * 128 * 8192 * 8192 // (2 * rows))
+        if c["new"] == 0:
+            room = min(room, math.isqrt(32 * 128 * 8192 * 8192 // (c["seqs"] * c["heads"] * c["dim"])))
+        c["longest"] = _spread(rng, 1, max(1, min(131072, room)))
+        c["mass"], c["lse"] = rng.random() < 0.4, rng.random() < 0.3
+    else:
+        c["seqs"] = _spread(rng, 1, 64)
+        c["longest"] = _spread(rng, 8, max(64, min(131072, 3 * 131072 * 8 * 128 // (2 * c["seqs"] * c["kv"] * c["dim"]))))
+        c["budget"] = rng.choice([max(1, c["longest"] - 1), _spread(rng, 1, c["longest"])])
+        c["sinks"] = min(c["budget"] // 4, rng.choice([0, 1, 4]))
+        c["recent"] = min(c["budget"] // 2, _spread(rng, 1, 512))
+        c["even"] = rng.random() < 0.5
+    return c
+
+
+def _lengths(case):
+    """(length after the call, new tokens) of each sequence; the first has the longest."""
+    r = random.Random(case["mix"])
+    lens = [case["longest"]] + [case["longest"] if case.get("even") else r.randint(max(1, case["longest"] // 4), case["longest"])
+                                for _ in range(case["seqs"] - 1)]
+    if case["op"] == "evict":
+        return lens, [0] * len(lens)
+    new = case["new"]
+    if new == 1:
+        return lens, [1] * len(lens)
+    if new == 0:
+        return lens, list(lens)
+    return lens, [max(1, min(n, r.randint(new - new // 3, new))) for n in lens]
+
+
+# --------------------------------------------------------- the plain 4-bit form
+def _quantize(x):
+    """E2M1 codes [..., D/2] and E8M0 scales [..., D/32] of x [..., D]."""
+    b = x.float().unflatten(-1, (-1, 32))
+    bits = b.abs().amax(-1).view(torch.int32)
+    # the least power of two with amax < 7 * 2^e: no value is further than half a step off
+    scale = ((bits >> 23) - 2 + ((bits & 0x7FFFFF) >= 0x600000)).clamp(1, 252)
+    y = b * (254 - scale).bitwise_left_shift(23).view(torch.float32)[..., None]
+    a = y.abs()
+    code = ((a > 0.25).byte() + (a >= 0.75).byte() + (a > 1.25).byte() + (a >= 1.75).byte() + (a > 2.5).byte()
+            + (a >= 3.5).byte() + (a > 5.0).byte() + 8 * torch.signbit(y).byte()).flatten(-2)
+    return code[..., 0::2] | (code[..., 1::2] << 4), scale.byte()
+
+
+_GRID = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0]
+
+
+def _values(codes, scales):
+    """float32 values [..., D] of codes [..., D/2] and scales [..., D/32]."""
+    pair = torch.tensor([[_GRID[b & 15], _GRID[b >> 4]] for b in range(256)], device=codes.device)
+    x = pair[codes.int()].flatten(-2)
+    s = (scales.int() << 23).view(torch.float32)
+    return (x.unflatten(-1, (-1, 32)) * s[..., None]).flatten(-2)
+
+
+def _sections(pages, dim):
+    """Views of a page pool [N, H, bytes]: K codes, V codes, K scales, V scales."""
+    n, h, size = pages.shape
+    p = size * 16 // (17 * dim)
+    a, b = p * dim // 2, p * dim // 32
+    return (pages[..., :a].unflatten(-1, (p, dim // 2)),
+            pages[..., a:2 * a].unflatten(-1, (p // 4, 16, 4, dim // 32)),
+            pages[..., 2 * a:2 * a + b].unflatten(-1, (p, dim // 32)),
+            pages[..., 2 * a + b:].unflatten(-1, (p // 4, dim // 32, 4)))
+
+
+def _put(pages, dim, pg, slot, k, v):
+    """Rows k, v [T, H, D] into slots `slot` of pages `pg`."""
+    kc, vc, ks, vs = _sections(pages, dim)
+    kc[pg, :, slot], ks[pg, :, slot] = _quantize(k)
+    code, scale = _quantize(v)
+    vc[pg, :, slot // 4, :, slot % 4] = code.unflatten(-1, (16, dim // 32))
+    vs[pg, :, slot // 4, :, slot % 4] = scale
+
+
+def _get(pages, dim, pg, slot):
+    kc, vc, ks, vs = _sections(pages, dim)
+    k = _values(kc[pg, :, slot], ks[pg, :, slot])
+    v = _values(vc[pg, :, slot // 4, :, slot % 4].flatten(-2), vs[pg, :, slot // 4, :, slot % 4])
+    return k, v
+
+
+def _page_values(pages, dim, table):
+    """float32 K and V [B, H, slots, D] behind a block table [B, M]."""
+    kc, vc, ks, vs = _sections(pages, dim)
+    k = _values(kc[table], ks[table])                                    # [B, M, H, P, D]
+    v = _values(vc[table].transpose(-3, -2).flatten(-2), vs[table].transpose(-2, -1))
+    return k.transpose(1, 2).flatten(2, 3), v.flatten(3, 4).transpose(1, 2).flatten(2, 3)
+
+
+def _rows(cu, count):
+    """(sequence, index within it) of every packed row."""
+    row = torch.arange(count, device=cu.device)
+    seq = torch.searchsorted(cu[1:].long(), row, right=True)
+    return seq, row - cu.long()[seq]
+
+
+# -------------------------------------------------------------------- inputs
+def _cache_rows(g, shape, dim, scales):
+    """Rows with channel scales of their own (some large) and a common offset, as keys have them."""
+    return (torch.randn(*shape, dim, generator=g, device=DEV) + 0.3) * scales
+
+
+def _channel_scales(g, kv, dim):
+    s = torch.exp(0.4 * torch.randn(kv, 1, dim, generator=g, device=DEV))
+    return torch.where(torch.rand(kv, 1, dim, generator=g, device=DEV) < 0.02, 6.0 * s, s)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV).manual_seed(1000003 * seed + case["mix"] % 999983)
+    kv, dim, page = case["kv"], case["dim"], case["page"]
+    lens, new = _lengths(case)
+    per = [-(-n // page) for n in lens]
+    total, most = sum(per) + 3, max(per)
+    order = torch.randperm(total, generator=g, device=DEV).to(torch.int32)
+    table = torch.zeros(len(lens), most, dtype=torch.int32, device=DEV)
+    at = 0
+    for b, n in enumerate(per):
+        table[b, :n] = order[at:at + n]
+        at += n
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    rows = cu[-1]
+    s = {"op": case["op"], "kv": kv, "dim": dim, "page": page, "table": table, "lens": ints(lens), "cu": ints(cu),
+         "rows": rows, "longest": max(lens), "most_new": max(new)}
+    ksc, vsc = _channel_scales(g, kv, dim), _channel_scales(g, kv, dim)
+    kc, ks = _quantize(_cache_rows(g, (total, kv, page), dim, ksc))
+    vc, vs = _quantize(_cache_rows(g, (total, kv, page), dim, vsc))
+    vc = vc.unflatten(-1, (16, dim // 32)).unflatten(2, (-1, 4)).transpose(3, 4)
+    vs = vs.unflatten(2, (-1, 4)).transpose(3, 4)
+    s["pages"] = torch.cat([kc.flatten(2), vc.flatten(2), ks.flatten(2), vs.flatten(2)], dim=2)
+    if case["op"] == "append":
+        # K and V as slices of one projection's rows; the first heads stand for the queries
+        x = _cache_rows(g, (rows, 3 * kv), dim, torch.cat([ksc, ksc, vsc])[:, 0]).to(TYPES[case["type"]])
+        s["k"], s["v"] = x[:, kv:2 * kv], x[:, 2 * kv:]
+        s["out_type"] = torch.float16 if case["type"] == "fp16" else torch.bfloat16
+        s["positions"] = torch.cat([torch.arange(n - m, n, device=DEV) for n, m in zip(lens, new)]).to(torch.int32) * 2
+        s["mass"] = torch.rand(total, kv, page, generator=g, device=DEV)
+        s["pos"] = torch.zeros(total, kv, page, dtype=torch.int32, device=DEV)
+    elif case["op"] == "read":
+        s["out_type"] = TYPES[case["type"]]
+    elif case["op"] == "attend":
+        s["q"] = (1.2 * torch.randn(rows, case["heads"], dim, generator=g, device=DEV)).to(TYPES[case["type"]])
+        s["scale"] = 1.0 / math.sqrt(dim)
+        s["lse"] = case["lse"]
+        if case["mass"]:
+            s["mass"] = 4.0 * torch.rand(total, kv, page, generator=g, device=DEV)
+            s["mass_out"] = torch.zeros_like(s["mass"])
+    else:
+        # weights spread over orders of magnitude, some slots never attended to; order lost by earlier evictions
+        w = torch.exp(2.0 * torch.randn(total, kv, page, generator=g, device=DEV))
+        s["mass"] = torch.where(torch.rand(total, kv, page, generator=g, device=DEV) < 0.05, 0.0, w)
+        s["pos"] = torch.zeros(total, kv, page, dtype=torch.int32, device=DEV)
+        for b, n in enumerate(per):
+            p = 2 * torch.rand(kv, n * page, generator=g, device=DEV).argsort(1) + torch.randint(0, 2, (kv, n * page), generator=g, device=DEV)
+            s["pos"][table[b, :n].long()] = p.to(torch.int32).unflatten(1, (n, page)).transpose(0, 1)
+        s["next_pos"] = ints([2 * n * page for n in per])
+        s["mass_out"], s["pos_out"] = torch.zeros_like(s["mass"]), torch.zeros_like(s["pos"])
+        s["budget"], s["sinks"], s["recent"] = case["budget"], case["sinks"], case["recent"]
+    return s
+
+
+# ------------------------------------------------------------------ the passes
+def _slots(s):
+    """Page and slot in it of every packed row, rows of sequence b ending at its length."""
+    seq, i = _rows(s["cu"], s["rows"])
+    cu = s["cu"].long()
+    at = s["lens"].long()[seq] - (cu[1:] - cu[:-1])[seq] + i
+    return s["table"].long()[seq, at // s["page"]], at % s["page"]
+
+
+def _append_plain(s):
+    pg, slot = _slots(s)
+    _put(s["pages"], s["dim"], pg, slot, s["k"], s["v"])
+    s["mass"][pg, :, slot] = 0.0
+    s["pos"][pg, :, slot] = s["positions"][:, None].expand(-1, s["kv"])
+    k, v = _get(s["pages"], s["dim"], pg, slot)
+    return {"k": k.to(s["out_type"]), "v": v.to(s["out_type"]), "mass": s["mass"], "pos": s["pos"]}
+
+
+def _append_own(s):
+    import lossless_kv_cache_splitzip_amd as sz
+    sz.kv4_append(s["pages"], s["k"], s["v"], s["table"], s["lens"], cu=s["cu"], positions=s["positions"],
+                  mass=s["mass"], pos=s["pos"])
+    k, v = sz.kv4_read(s["pages"], s["table"], s["lens"], s["dim"], cu=s["cu"], n_tokens=s["rows"],
+                       dtype=s["out_type"])
+    return {"k": k, "v": v, "mass": s["mass"], "pos": s["pos"]}
+
+
+def _read_plain(s):
+    pg, slot = _slots(s)
+    k, v = _get(s["pages"], s["dim"], pg, slot)
+    return {"k": k.to(s["out_type"]), "v": v.to(s["out_type"])}
+
+
+def _read_own(s):
+    import lossless_kv_cache_splitzip_amd as sz
+    k, v = sz.kv4_read(s["pages"], s["table"], s["lens"], s["dim"], cu=s["cu"], n_tokens=s["rows"],
+                       dtype=s["out_type"])
+    return {"k": k, "v": v}
+
+
+def _attend_plain(s):
+    q, kv, dim, table = s["q"], s["kv"], s["dim"], s["table"].long()
+    heads = q.shape[1]
+    group = heads // kv
+    k, v = _page_values(s["pages"], dim, table)                          # [B, H, L, D]
+    seqs, length = k.shape[0], k.shape[2]
+    seq, i = _rows(s["cu"], s["rows"])
+    cu, lens = s["cu"].long(), s["lens"].long()
+    pad = q.new_zeros(seqs, s["most_new"], heads, dim, dtype=torch.float32)
+    pad[seq, i] = q.float()
+    pad = pad.unflatten(2, (kv, group)).permute(0, 2, 1, 3, 4).flatten(2, 3)  # [B, H, rows, D]
+    logit = torch.matmul(pad, k.transpose(2, 3)) * s["scale"]
+    step = torch.arange(s["most_new"], device=q.device)
+    count = cu[1:] - cu[:-1]
+    last = (lens - count)[:, None] + step                                # [B, Q]: the newest slot that a row sees
+    last = torch.where(step < count[:, None], last, -1)
+    seen = torch.arange(length, device=q.device) <= last[..., None]
+    seen = seen[:, None, :, None].expand(-1, 1, -1, group, -1).flatten(2, 3)  # [B, 1, rows, L]
+    logit = torch.where(seen, logit, -math.inf)
+    top = logit.amax(-1, keepdim=True)
+    p = torch.exp(logit - torch.where(top == -math.inf, 0.0, top))
+    del logit
+    total = p.sum(-1, keepdim=True)
+    p = p / torch.where(total == 0, 1.0, total)
+    o = torch.matmul(p, v).unflatten(2, (-1, group)).permute(0, 2, 1, 3, 4).flatten(2, 3)
+    r = {"out": o[seq, i].to(q.dtype)}
+    if s["lse"]:
+        lse = (top + torch.log(total))[..., 0].unflatten(2, (-1, group)).permute(0, 2, 1, 3).flatten(2, 3)
+        r["lse"] = lse[seq, i]
+    if "mass" in s:
+        add = p.sum(2).unflatten(2, (-1, s["page"])).transpose(1, 2)     # [B, M, H, P]
+        at = torch.arange(length, device=q.device).unflatten(0, (-1, s["page"])) < lens[:, None, None]
+        b, m, off = at.nonzero(as_tuple=True)
+        pg = table[b, m]
+        s["mass_out"][pg, :, off] = s["mass"][pg, :, off] + add[b, m, :, off]
+        r["mass"] = s["mass_out"]
+    return r
+
+
+def _attend_own(s):
+    import lossless_kv_cache_splitzip_amd as sz
+    out = sz.kv4_attention(s["q"], s["pages"], s["table"], s["lens"], cu=s["cu"], max_new=s["most_new"],
+                           scale=s["scale"], max_len=s["longest"], mass=s.get("mass"), mass_out=s.get("mass_out"),
+                           return_lse=s["lse"])
+    r = {"out": out[0], "lse": out[1]} if s["lse"] else {"out": out}
+    if "mass" in s:
+        r["mass"] = s["mass_out"]
+    return r
+
+
+def _evict_plain(s):
+    table, lens, page, budget = s["table"].long(), s["lens"].long(), s["page"], s["budget"]
+    rows = lambda x: x[table].transpose(1, 2).flatten(2, 3)  # noqa: E731  [B, H, L]
+    mass, pos = rows(s["mass"]), rows(s["pos"])
+    slot = torch.arange(mass.shape[2], device=mass.device)
+    live = (slot < lens[:, None])[:, None]
+    safe = (pos < s["sinks"]) | (pos >= (s["next_pos"] - s["recent"])[:, None, None])
+    key = torch.where(safe, math.inf, mass)
+    key = torch.where(live, key, -math.inf)
+    place = key.argsort(dim=2, descending=True, stable=True).argsort(dim=2)
+    keep = live & (place < budget)
+    left = lens.clamp(max=budget)
+    low = slot < left[:, None, None]
+    hole, mover = live & low & ~keep, keep & ~low
+    # the i-th hole takes the i-th kept slot behind the new end
+    b, h, to = hole.nonzero(as_tuple=True)
+    b2, h2, source = mover.nonzero(as_tuple=True)
+    pg, off, pg2, off2 = table[b, to // page], to % page, table[b2, source // page], source % page
+    for_all = low.expand_as(mass).nonzero(as_tuple=True)
+    bp, hp, sp = for_all
+    pp, po = table[bp, sp // page], sp % page
+    s["mass_out"][pp, hp, po] = s["mass"][pp, hp, po]
+    s["pos_out"][pp, hp, po] = s["pos"][pp, hp, po]
+    s["mass_out"][pg, h, off] = s["mass"][pg2, h2, off2]
+    s["pos_out"][pg, h, off] = s["pos"][pg2, h2, off2]
+    kc, vc, ks, vs = _sections(s["pages"], s["dim"])
+    kc[pg, h, off], ks[pg, h, off] = kc[pg2, h2, off2], ks[pg2, h2, off2]
+    vc[pg, h, off // 4, :, off % 4] = vc[pg2, h2, off2 // 4, :, off2 % 4]
+    vs[pg, h, off // 4, :, off % 4] = vs[pg2, h2, off2 // 4, :, off2 % 4]
+    # pages are moved, not computed: they come as the bytes that they are
+    return {"lens": left.to(torch.int32), "mass": s["mass_out"], "pos": s["pos_out"], "pages": s["pages"]}
+
+
+def _evict_own(s):
+    import lossless_kv_cache_splitzip_amd as sz
+    lens, _, _ = sz.kv4_evict(s["pages"], s["table"], s["lens"], s["mass"], s["pos"], s["next_pos"], s["dim"],
+                              budget=s["budget"], sinks=s["sinks"], recent=s["recent"], max_len=s["longest"],
+                              lens_out=torch.empty_like(s["lens"]), mass_out=s["mass_out"], pos_out=s["pos_out"])
+    return {"lens": lens, "mass": s["mass_out"], "pos": s["pos_out"], "pages": s["pages"]}
+
+
+def run(state):
+    if own:
+        return {"append": _append_own, "read": _read_own, "attend": _attend_own, "evict": _evict_own}[state["op"]](state)
+    return {"append": _append_plain, "read": _read_plain, "attend": _attend_plain, "evict": _evict_plain}[state["op"]](state)
+
+
+# ------------------------------------------------------------------- the floors
+def work(case):
+    lens, new = _lengths(case)
+    kv, dim = case["kv"], case["dim"]
+    row = 2 * kv * dim                      # K and V values of one token
+    held = row * 17 // 32                   # their bytes in the cache
+    rows, batch = sum(new), len(lens)
+    index = 4 * (2 * batch + 1) + 4 * sum(-(-n // case["page"]) for n in lens)
+    if case["op"] == "append":
+        size = 1 if case["type"] == "e5m2" else 2
+        # in, put away with weight and position, then read and out as 16 bits
+        return {"bytes": rows * (row * size + 2 * held + 8 * kv + 4 + row * 2) + index, "flops": rows * row * 4}
+    if case["op"] == "read":
+        return {"bytes": rows * (held + row * 2) + index, "flops": rows * row}
+    if case["op"] == "attend":
+        heads = case["heads"]
+        pairs = sum(m * (n - m) + m * (m + 1) // 2 for n, m in zip(lens, new))
+        size = sum(lens) * held + rows * heads * dim * 2 * 2 + index
+        size += (sum(lens) * kv * 8 if case["mass"] else 0) + (rows * heads * 4 if case["lse"] else 0)
+        return {"bytes": size, "flops": 4 * dim * heads * pairs}
+    # eviction: every weight and position once, the new ones written; a kept token behind the new end is read and
+    # written once. How many those are hangs on the weights: where they say nothing of the place, a share
+    # budget / length of the slots behind the new end
+    size = index + 4 * batch
+    for n in lens:
+        left = min(n, case["budget"])
+        moved = (n - left) * left // n
+        size += kv * (8 * n + 8 * left) + moved * held * 2
+    return {"bytes": size, "flops": 0}
+
+
+# ------------------------------------------------- the definitions in 64 bits
+def _byte_values(block, dim, t, which):
+    """float64 rows `t` [N] of K (which = 0) or V (1) of pages' bytes block [N, bytes], one page a row."""
+    page = block.shape[1] * 16 // (17 * dim)
+    c = torch.arange(dim, device=block.device)
+    half, n32 = page * dim // 2, dim // 32
+    t = t[:, None]
+    if which == 0:
+        code, scale = t * (dim // 2) + c // 2, 2 * half + t * n32 + c // 32
+    else:
+        wide = dim // 16
+        code = half + ((t // 4 * 16 + c // wide) * 4 + t % 4) * n32 + c % wide // 2
+        scale = 2 * half + page * n32 + (t // 4 * n32 + c // 32) * 4 + t % 4
+    x = (block.gather(1, code).long() >> (4 * (c % 2))) & 15
+    e, m = (x >> 1) & 3, x & 1
+    mag = torch.where(e == 0, 0.5 * m.double(), torch.ldexp(1.0 + 0.5 * m.double(), (e - 1).double()))
+    value = torch.ldexp(mag, block.gather(1, scale).double() - 127.0)
+    return torch.where(x >= 8, -value, value)
+
+
+def _nearest(x):
+    """The 4-bit form's float64 values of x [..., D], by distance to every representable value."""
+    b = x.double().unflatten(-1, (-1, 32))
+    f, e = torch.frexp(b.abs().amax(-1, keepdim=True))
+    e = torch.where(f < 0.875, e - 3, e - 2).clamp(-126, 125).double()
+    y = torch.ldexp(b, -e)
+    grid = torch.tensor([0.0, 1.0, 2.0, 4.0, 0.5, 1.5, 3.0, 6.0], dtype=torch.float64, device=x.device)  # even codes first: ties go to them
+    near = grid[(y.abs()[..., None] - grid).abs().argmin(-1)]
+    return torch.ldexp(torch.where(y < 0, -near, near), e).flatten(-2)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    lens, new = _lengths(case)
+    kv, dim, page = s["kv"], s["dim"], s["page"]
+    if case["op"] == "append":
+        mass, pos, at = s["mass"].double(), s["pos"].clone(), 0
+        for b, (n, m) in enumerate(zip(lens, new)):
+            where = torch.arange(n - m, n, device=DEV)
+            pg = s["table"][b].long()[where // page]
+            mass[pg, :, where % page] = 0.0
+            pos[pg, :, where % page] = s["positions"][at:at + m, None].expand(m, kv)
+            at += m
+        step = max(1, (1 << 26) // (kv * dim))
+        part = lambda x: torch.cat([_nearest(x[i:i + step].float()) for i in range(0, x.shape[0], step)])  # noqa: E731
+        return {"k": part(s["k"]), "v": part(s["v"]), "mass": mass, "pos": pos}
+    if case["op"] == "read":
+        both = []
+        for which in (0, 1):
+            rows = []
+            for b, (n, m) in enumerate(zip(lens, new)):
+                where = torch.arange(n - m, n, device=DEV)
+                pg = s["table"][b].long()[where // page]
+                rows.append(torch.stack([_byte_values(s["pages"][pg, h], dim, where % page, which) for h in range(kv)], 1))
+            both.append(torch.cat(rows))
+        return {"k": both[0], "v": both[1]}
+    if case["op"] == "attend":
+        heads = case["heads"]
+        group = heads // kv
+        if max(lens) * max(new) * group * 8 > 40e9:
+            return None
+        out = torch.zeros(s["rows"], heads, dim, dtype=torch.float64, device=DEV)
+        lse = torch.full((s["rows"], heads), -math.inf, dtype=torch.float64, device=DEV)
+        mass = s["mass_out"].double() if case["mass"] else None
+        at = 0
+        for b, (n, m) in enumerate(zip(lens, new)):
+            where = torch.arange(n, device=DEV)
+            pg, off = s["table"][b].long()[where // page], where % page
+            hidden = where[None, :] > (n - m + torch.arange(m, device=DEV))[:, None]
+            for h in range(kv):
+                k, v = (_byte_values(s["pages"][pg, h], dim, off, w) for w in (0, 1))
+                q = s["q"][at:at + m, h * group:(h + 1) * group].double()
+                x = (q.reshape(m * group, dim) @ k.T).div_(math.sqrt(dim)).reshape(m, group, n)
+                x.masked_fill_(hidden[:, None, :], -math.inf)
+                z = torch.logsumexp(x, -1)
+                p = x.sub_(z[..., None]).exp_()
+                out[at:at + m, h * group:(h + 1) * group] = (p.reshape(m * group, n) @ v).reshape(m, group, dim)
+                lse[at:at + m, h * group:(h + 1) * group] = z
+                if case["mass"]:
+                    mass[pg, h, off] = s["mass"][pg, h, off].double() + p.sum((0, 1))
+            at += m
+        r = {"out": out}
+        if case["lse"]:
+            r["lse"] = lse
+        if case["mass"]:
+            r["mass"] = mass
+        return r
+    mass_out, pos_out, pages = s["mass_out"].double(), s["pos_out"].clone(), s["pages"].clone()
+    for b, n in enumerate(lens):
+        where = torch.arange(n, device=DEV)
+        pg, off = s["table"][b].long()[where // page], where % page
+        left = min(n, case["budget"])
+        for h in range(kv):
+            w, p = s["mass"][pg, h, off].double(), s["pos"][pg, h, off].long()
+            w[(p < case["sinks"]) | (p >= int(s["next_pos"][b]) - case["recent"])] = math.inf
+            kept = torch.sort(w, descending=True, stable=True).indices[:left].sort().values
+            behind = kept[kept >= left]
+            free = torch.ones(left, dtype=torch.bool, device=DEV)
+            free[kept[kept < left]] = False
+            free = free.nonzero()[:, 0]
+            source = where[:left].clone()
+            source[free] = behind
+            mass_out[pg[:left], h, off[:left]] = s["mass"][pg[source], h, off[source]].double()
+            pos_out[pg[:left], h, off[:left]] = s["pos"][pg[source], h, off[source]]
+            c = torch.arange(dim, device=DEV)
+            half, n32, wide = page * dim // 2, dim // 32, dim // 16
+            spot = lambda t: torch.cat([t * (dim // 2) + c[::2] // 2, 2 * half + t * n32 + c[::32] // 32,  # noqa: E731
+                                        half + ((t // 4 * 16 + c[::2] // wide) * 4 + t % 4) * n32 + c[::2] % wide // 2,
+                                        2 * half + page * n32 + (t // 4 * n32 + c[::32] // 32) * 4 + t % 4], 1)
+            to, source = off[free][:, None], off[behind][:, None]
+            pages[pg[free][:, None], h, spot(to)] = s["pages"][pg[behind][:, None], h, spot(source)]
+    return {"lens": torch.tensor([min(n, case["budget"]) for n in lens], dtype=torch.int32, device=DEV),
+            "mass": mass_out, "pos": pos_out, "pages": pages}
