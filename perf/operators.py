@@ -447,11 +447,16 @@ def _nearest(x):
     """The 4-bit form's float64 values of x [..., D], by distance to every representable value."""
     b = x.double().unflatten(-1, (-1, 32))
     f, e = torch.frexp(b.abs().amax(-1, keepdim=True))
-    e = torch.where(f < 0.875, e - 3, e - 2).clamp(-126, 125).double()
-    y = torch.ldexp(b, -e)
-    grid = torch.tensor([0.0, 1.0, 2.0, 4.0, 0.5, 1.5, 3.0, 6.0], dtype=torch.float64, device=x.device)  # even codes first: ties go to them
-    near = grid[(y.abs()[..., None] - grid).abs().argmin(-1)]
-    return torch.ldexp(torch.where(y < 0, -near, near), e).flatten(-2)
+    e = torch.where(f < 0.875, e - 3, e - 2).clamp(-126, 125).long()
+    power = lambda n: ((n + 1023) << 52).view(torch.float64)  # noqa: E731  exact, as ldexp on the GPU is not
+    y = b * power(-e)
+    grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64, device=x.device)
+    a = y.abs()
+    low = (a[..., None] >= grid[1:]).sum(-1)
+    high = (low + 1).clamp(max=7)
+    down, up = a - grid[low], grid[high] - a
+    near = grid[torch.where((up < down) | ((up == down) & (low % 2 == 1)), high, low)]  # a tie goes to the even code
+    return (torch.where(y < 0, -near, near) * power(e)).flatten(-2)
 
 
 def exact(case, seed):
