@@ -73,7 +73,8 @@ enum {
   SPLITZIP_E_CODEBOOK = -3, /* codebook entries repeated or out of range for the dtype */
   SPLITZIP_E_CORRUPT = -4,  /* stream fails validation (reported through d_status) */
   SPLITZIP_E_HIP = -5,      /* a HIP launch failed */
-  SPLITZIP_E_TOO_LARGE = -6 /* input beyond splitzip_compress_static's limit */
+  SPLITZIP_E_TOO_LARGE = -6, /* input beyond splitzip_compress_static's limit */
+  SPLITZIP_E_NONFINITE = -7 /* a NaN or infinity met by splitzip_kv4_append (reported through d_status) */
 };
 
 /* Offline calibration (technical summary, "Metodologia / Codificacion de
@@ -292,6 +293,164 @@ int splitzip_pipeline_transfer(int dtype, const void* d_in, size_t n_elems, cons
                                int compress, void* d_work, size_t d_work_bytes, void* h_link, size_t h_link_bytes,
                                void* d_out, int32_t* d_status, uint64_t* h_group_bytes,
                                const hipStream_t streams[4]);
+
+/* ---- 4-bit KV cache -------------------------------------------------------
+ * Where the codec carries a cache to the decode side bit for bit, these calls
+ * keep it there in 4 bits, attend over it and keep it within a budget.  The
+ * cache is paged: splitzip_kv4_append puts K and V rows away (the encoder),
+ * splitzip_kv4_read gives them back (the decoder), splitzip_kv4_attention
+ * reads them in place and splitzip_kv4_evict drops the slots that drew the
+ * least attention.
+ *
+ * Values.  The OCP microscaling form: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 and their negatives; code bit 3 is the sign) in blocks of 32 consecutive
+ * channels of one token of one head, with one E8M0 scale byte s per block: a
+ * value is element * 2^(s - 127).  The encoder takes the least exponent e with
+ * max|x| < 7 * 2^e, s = e + 127 clamped to 1..252, and rounds every x / 2^e to
+ * the nearest element, ties to the even code, beyond 6 to 6: no element is
+ * further off than half its step (2^e at most), and no value of 252 or below
+ * overflows BF16.
+ *
+ * A page holds page_tokens consecutive slots of every head; the bytes of one
+ * head in it are contiguous (P = page_tokens, D = head_dim, 17/16 P D bytes,
+ * even channel in a byte's low nibble):
+ *   K codes   [P][D/2]
+ *   V codes   [P/4][16][4][D/32]: token / 4, channel / (D/16), token % 4,
+ *             bytes of the D/16 channels
+ *   K scales  [P][D/32]
+ *   V scales  [P/4][D/32][4]
+ * d_pages is [n_pages][n_heads][splitzip_kv4_page_bytes].  Side arrays, where
+ * a call takes them, are [n_pages][n_heads][page_tokens]: d_mass (float), the
+ * attention weight a slot has drawn so far, and d_pos (int32), the position of
+ * its token in the text (what the keys were rotated by, say).
+ *
+ * A batch names its sequences' pages by a block table and holds, packed one
+ * sequence after the other, the rows that a call is about: sequence b has the
+ * rows d_cu[b] .. d_cu[b + 1] - 1, which stand for its LAST slots, d_lens[b] -
+ * (number of rows) up to d_lens[b] - 1.  d_lens counts the rows of the call.
+ * Two sequences may share pages that are only read.  A sequence whose length,
+ * rows or page numbers are out of range is reported through d_status
+ * (SPLITZIP_E_CORRUPT, sticky as in splitzip_decompress) and its results are
+ * unspecified or left as they were; every access stays inside the arrays.
+ * Packed rows of no sequence are left as they were. */
+typedef struct {
+  void* d_pages;        /* 16-byte aligned */
+  uint32_t n_pages;     /* 1 .. 2^31 - 1 */
+  uint32_t n_heads;     /* KV heads, 1 .. 1024 */
+  uint32_t head_dim;    /* 64, 128 or 256 */
+  uint32_t page_tokens; /* 16, 32, 64, 128 or 256 */
+} splitzip_kv4_cache;
+
+typedef struct {
+  const int32_t* d_table; /* [n_seqs][table_stride] page numbers */
+  size_t table_stride;    /* entries between rows, >= ceil(max_len / page_tokens) */
+  const int32_t* d_lens;  /* [n_seqs] slots in use */
+  const int32_t* d_cu;    /* [n_seqs + 1] first packed row of each sequence; NULL: one row each (n_rows == n_seqs) */
+  uint32_t n_seqs;        /* 0 .. 65535 */
+  uint32_t max_len;       /* no length is larger; up to 2^30 */
+  uint32_t max_new;       /* no sequence has more rows; <= n_rows */
+  uint32_t n_rows;        /* rows of the packed tensors; up to 2^30 */
+} splitzip_kv4_batch;
+
+/* Element types of the 4-bit cache's rows besides splitzip_dtype. */
+enum { SPLITZIP_KV4_FP16 = 3 };
+
+/* Bytes of one head in one page, 0 for a head_dim or page_tokens outside the
+ * lists above. */
+size_t splitzip_kv4_page_bytes(uint32_t head_dim, uint32_t page_tokens);
+
+/* Encode rows into the batch's slots.  One launch.
+ *   dtype        SPLITZIP_BF16, SPLITZIP_KV4_FP16 or SPLITZIP_FP8_E5M2.
+ *   d_k, d_v     [n_rows][n_heads][head_dim] with strides in elements between
+ *                rows and between heads, multiples of 8 (channels contiguous);
+ *                aligned to 8 elements.
+ *   d_positions  optional [n_rows]: the tokens' positions for d_pos; NULL: the
+ *                slot's number.
+ *   d_mass       optional: the rows' slots are set to 0.
+ *   d_pos        optional: the rows' slots get their positions.
+ * A NaN is stored as 0 and an infinity as the block's largest magnitude (its
+ * scale is that of the finite values); d_status then gets
+ * SPLITZIP_E_NONFINITE unless it already holds an error.  A sequence with
+ * more rows than slots is an error of the batch.  Two rows that meet in one
+ * slot (pages shared by mistake) leave either's bytes.
+ * Returns SPLITZIP_OK, SPLITZIP_E_INVALID or SPLITZIP_E_HIP. */
+int splitzip_kv4_append(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch, int dtype, const void* d_k,
+                        size_t k_row_stride, size_t k_head_stride, const void* d_v, size_t v_row_stride,
+                        size_t v_head_stride, const int32_t* d_positions, float* d_mass, int32_t* d_pos,
+                        int32_t* d_status, hipStream_t stream);
+
+/* Decode the batch's slots into rows d_k, d_v [n_rows][n_heads][head_dim]
+ * (contiguous, 16-byte aligned; either may be NULL).  dtype: SPLITZIP_BF16
+ * (exact) or SPLITZIP_KV4_FP16 (exact from 2^-24 to 65504, rounded to nearest
+ * or infinite outside).  A sequence with more rows than slots is an error of
+ * the batch.  One launch.  Returns SPLITZIP_OK, SPLITZIP_E_INVALID or
+ * SPLITZIP_E_HIP. */
+int splitzip_kv4_read(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch, int dtype, void* d_k,
+                      void* d_v, int32_t* d_status, hipStream_t stream);
+
+/* Bytes of d_work of splitzip_kv4_attention (the partial results of the
+ * splits of the long axis); with_mass: d_mass_out is given.  0 for arguments
+ * that the call refuses. */
+size_t splitzip_kv4_attention_work_bytes(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch,
+                                         uint32_t n_q_heads, int with_mass);
+
+/* Causal attention of packed queries over the cache, heads grouped: query
+ * head a reads KV head a / (n_q_heads / n_heads).  Row i of the m rows of a
+ * sequence of length n sees the slots j <= n - m + i; its own K and V are in
+ * the cache (appended before).  With x_ij = scale * q_i . k_j,
+ *   p_ij = exp(x_ij) / sum_j exp(x_ij),  out_i = sum_j p_ij v_j,
+ *   lse_i = log sum_j exp(x_ij)
+ * and a row that sees no slot (m > n) gives out 0 and lse -infinity.  m is 1
+ * when tokens are generated one by one, a few when drafts are checked, long
+ * for prompts and chunks of them.
+ *   dtype      of d_q and d_out: SPLITZIP_BF16 or SPLITZIP_KV4_FP16.
+ *   d_q        [n_rows][n_q_heads][head_dim] with strides in elements between
+ *              rows and heads, multiples of 8; 16-byte aligned; not overlapped
+ *              by what the call writes.
+ *   n_q_heads  a multiple of n_heads, at most 64 query heads per KV head.
+ *   scale      finite and above 0.
+ *   d_out      [n_rows][n_q_heads][head_dim], contiguous, 16-byte aligned.
+ *   d_lse      optional float [n_rows][n_q_heads].
+ *   d_mass, d_mass_out  optional, both or none: for every slot of a sequence
+ *              d_mass_out = d_mass + the sum of p over the sequence's rows and
+ *              the head's queries; they may be one array.  Sums run in a fixed
+ *              order: results repeat bit for bit.  Sequences that share pages
+ *              here leave one of their sums in them.
+ *   d_work     splitzip_kv4_attention_work_bytes bytes, 256-byte aligned,
+ *              overwritten; calls that may overlap need one each.
+ * Weights and sums are held in 32 bits.  Only launches kernels, as the codec's
+ * calls.  Returns SPLITZIP_OK, SPLITZIP_E_INVALID, SPLITZIP_E_CAPACITY (d_work
+ * too small) or SPLITZIP_E_HIP. */
+int splitzip_kv4_attention(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch, int dtype,
+                           const void* d_q, size_t q_row_stride, size_t q_head_stride, uint32_t n_q_heads, float scale,
+                           void* d_out, float* d_lse, const float* d_mass, float* d_mass_out, void* d_work,
+                           size_t work_bytes, int32_t* d_status, hipStream_t stream);
+
+/* Bytes of d_work of splitzip_kv4_evict, 0 for arguments that it refuses. */
+size_t splitzip_kv4_evict_work_bytes(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch, uint32_t budget);
+
+/* Cut every sequence longer than `budget` to `budget` slots, each head for
+ * itself.  Kept are first the slots whose token position is below `sinks` or
+ * at least d_next_pos[b] - recent (all ranking equal), then those of the largest
+ * d_mass (a NaN ranks below -infinity), equal ones by the lowest slot.  Slots below the new
+ * length stay where they are: in ascending order, the i-th dropped slot below
+ * it receives the i-th kept slot at or beyond it (cache bytes, mass and
+ * position).  Attention does not depend on the order of past slots, so only
+ * those few tokens move; d_pos says which token a slot holds.
+ *   batch       d_cu, max_new and n_rows are not read.
+ *   sinks + recent <= budget, budget >= 1.
+ *   d_next_pos  [n_seqs] position that the sequence's next token will have.
+ *   d_lens_out  [n_seqs] min(length, budget); may be d_lens.
+ *   d_mass_out, d_pos_out  the slots below the new length; may be d_mass,
+ *               d_pos.  Other entries are left as they were.
+ *   d_work      splitzip_kv4_evict_work_bytes bytes, 256-byte aligned,
+ *               overwritten; calls that may overlap need one each.
+ * The sequences' pages must not be shared.  Returns SPLITZIP_OK,
+ * SPLITZIP_E_INVALID, SPLITZIP_E_CAPACITY or SPLITZIP_E_HIP. */
+int splitzip_kv4_evict(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch, uint32_t budget,
+                       uint32_t sinks, uint32_t recent, const int32_t* d_next_pos, const float* d_mass,
+                       const int32_t* d_pos, int32_t* d_lens_out, float* d_mass_out, int32_t* d_pos_out, void* d_work,
+                       size_t work_bytes, int32_t* d_status, hipStream_t stream);
 
 #ifdef __cplusplus
 }

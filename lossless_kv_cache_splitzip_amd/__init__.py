@@ -12,9 +12,11 @@ from ._native import (  # noqa: F401
     E_CORRUPT,
     E_HIP,
     E_INVALID,
+    E_NONFINITE,
     E_TOO_LARGE,
     EXPORTS,
     FP8_E5M2,
+    KV4_FP16,
     LIB_PATH,
     OK,
     VARIANT_TOP15_SENTINEL,
@@ -40,3 +42,17 @@ from ._native import (  # noqa: F401
     variant_compress,
     variant_decompress,
 )
+
+_KV4 = ("kv4_append", "kv4_attention", "kv4_evict", "kv4_page_bytes", "kv4_pages", "kv4_read")
+
+
+def __getattr__(name):
+    # the 4-bit cache's calls need torch from the start; the codec's import it when called
+    if name in _KV4:
+        from . import kv4
+        return getattr(kv4, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted([*globals(), *_KV4])

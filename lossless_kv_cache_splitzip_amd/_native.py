@@ -23,6 +23,8 @@ E_CODEBOOK = -3
 E_CORRUPT = -4
 E_HIP = -5
 E_TOO_LARGE = -6
+E_NONFINITE = -7
+KV4_FP16 = 3
 VARIANT_TOP15_SENTINEL = 1
 VARIANT_TOP8 = 2
 
@@ -40,7 +42,28 @@ EXPORTS = (
     "splitzip_pipeline_sizes",
     "splitzip_pipeline_transfer",
     "splitzip_compress_static",
+    "splitzip_kv4_page_bytes",
+    "splitzip_kv4_append",
+    "splitzip_kv4_read",
+    "splitzip_kv4_attention_work_bytes",
+    "splitzip_kv4_attention",
+    "splitzip_kv4_evict_work_bytes",
+    "splitzip_kv4_evict",
 )
+
+
+class KV4CacheDesc(ctypes.Structure):
+    """splitzip_kv4_cache."""
+    _fields_ = [("d_pages", ctypes.c_void_p), ("n_pages", ctypes.c_uint32), ("n_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("page_tokens", ctypes.c_uint32)]
+
+
+class KV4BatchDesc(ctypes.Structure):
+    """splitzip_kv4_batch."""
+    _fields_ = [("d_table", ctypes.c_void_p), ("table_stride", ctypes.c_size_t), ("d_lens", ctypes.c_void_p),
+                ("d_cu", ctypes.c_void_p), ("n_seqs", ctypes.c_uint32), ("max_len", ctypes.c_uint32),
+                ("max_new", ctypes.c_uint32), ("n_rows", ctypes.c_uint32)]
+
 
 _lib = None
 
@@ -89,6 +112,21 @@ def load():
     lib.splitzip_pipeline_transfer.restype = i32
     lib.splitzip_compress_static.argtypes = [i32, vp, sz, vp, u32, sz, vp, sz, vp, vp]
     lib.splitzip_compress_static.restype = i32
+    cp, bp, f32 = ctypes.POINTER(KV4CacheDesc), ctypes.POINTER(KV4BatchDesc), ctypes.c_float
+    lib.splitzip_kv4_page_bytes.argtypes = [u32, u32]
+    lib.splitzip_kv4_page_bytes.restype = sz
+    lib.splitzip_kv4_append.argtypes = [cp, bp, i32, vp, sz, sz, vp, sz, sz, vp, vp, vp, vp, vp]
+    lib.splitzip_kv4_append.restype = i32
+    lib.splitzip_kv4_read.argtypes = [cp, bp, i32, vp, vp, vp, vp]
+    lib.splitzip_kv4_read.restype = i32
+    lib.splitzip_kv4_attention_work_bytes.argtypes = [cp, bp, u32, i32]
+    lib.splitzip_kv4_attention_work_bytes.restype = sz
+    lib.splitzip_kv4_attention.argtypes = [cp, bp, i32, vp, sz, sz, u32, f32, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.splitzip_kv4_attention.restype = i32
+    lib.splitzip_kv4_evict_work_bytes.argtypes = [cp, bp, u32]
+    lib.splitzip_kv4_evict_work_bytes.restype = sz
+    lib.splitzip_kv4_evict.argtypes = [cp, bp, u32, u32, u32, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.splitzip_kv4_evict.restype = i32
     _lib = lib
     return lib
 

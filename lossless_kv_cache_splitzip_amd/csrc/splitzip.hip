@@ -2459,8 +2459,15 @@ const char* splitzip_status_string(int status) {
     case SPLITZIP_E_CORRUPT: return "corrupt stream";
     case SPLITZIP_E_HIP: return "HIP launch failure";
     case SPLITZIP_E_TOO_LARGE: return "input larger than splitzip_compress_static's workspace";
+    case SPLITZIP_E_NONFINITE: return "NaN or infinity in K or V";
     default: return "unknown status";
   }
 }
 
 }  // extern "C"
+
+// The 4-bit cache's calls, compiled in this unit so that a build of the
+// library's sources has the whole ABI.
+#include "kv4_codec.h"
+#include "kv4_attention.h"
+#include "kv4_evict.h"

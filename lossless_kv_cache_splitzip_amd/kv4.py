@@ -1,0 +1,301 @@
+"""The 4-bit KV cache from torch tensors (include/splitzip.h, "4-bit KV cache").
+
+Argument marshalling only, as in ``_native``: shapes, types and devices are
+checked here, every step runs in the library.  The tensors:
+
+* ``pages``  uint8 [n_pages, n_heads, page_bytes] (``kv4_pages`` allocates one),
+  ``kv4_page_bytes(head_dim, page_tokens)`` bytes a head;
+* ``table``  int32 [n_seqs, pages per sequence], ``lens`` int32 [n_seqs];
+* ``cu``     int32 [n_seqs + 1], the first packed row of each sequence; None
+  means one row each.  A sequence's rows stand for its last slots, and ``lens``
+  counts them;
+* ``mass`` float32 and ``pos`` int32 [n_pages, n_heads, page_tokens].
+
+``max_new`` (rows of one sequence) and ``max_len`` (slots of one sequence) are
+upper bounds known on the host; they default to all packed rows and to the
+table's width.  Tight bounds make launches smaller.  A ``stream`` given is used
+for the work and for what is allocated.  Nothing is synchronized.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _native as N
+
+_byref = ctypes.byref
+_HALF = {torch.bfloat16: N.BF16, torch.float16: N.KV4_FP16}
+_ROWS = {torch.bfloat16: N.BF16, torch.float16: N.KV4_FP16, torch.float8_e5m2: N.FP8_E5M2}
+_PAGES = (16, 32, 64, 128, 256)
+
+
+def kv4_page_bytes(head_dim: int, page_tokens: int) -> int:
+    """Bytes of one head in one page."""
+    n = int(N.load().splitzip_kv4_page_bytes(head_dim, page_tokens))
+    if n == 0:
+        raise N.SplitZipError(N.E_INVALID, "splitzip_kv4_page_bytes")
+    return n
+
+
+def kv4_pages(n_pages: int, n_heads: int, head_dim: int, page_tokens: int, device="cuda") -> torch.Tensor:
+    """An empty pool of pages."""
+    return torch.zeros(n_pages, n_heads, kv4_page_bytes(head_dim, page_tokens), dtype=torch.uint8, device=device)
+
+
+def _elsewhere(device, stream):
+    """The context to run in when the call is not for the current device and
+    stream, else None."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
+
+
+def _tensor(t, name, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr() or None
+
+
+def _optional(t, name, dtype, shape, device):
+    return None if t is None else _tensor(t, name, dtype, shape, device)
+
+
+def _pool(pages):
+    if not isinstance(pages, torch.Tensor) or not pages.is_cuda:
+        raise ValueError("pages must be a device tensor")
+    if pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
+        raise ValueError("pages must be a contiguous uint8 tensor [n_pages, n_heads, page_bytes]")
+    return pages.device
+
+
+def _cache(pages, head_dim):
+    n, heads, size = pages.shape
+    p = size * 16 // (17 * head_dim) if head_dim > 0 else 0
+    if head_dim not in (64, 128, 256) or p not in _PAGES or size * 16 != 17 * head_dim * p:
+        raise ValueError(f"pages of {size} bytes a head do not hold 16 to 256 tokens of head_dim {head_dim}")
+    return N.KV4CacheDesc(pages.data_ptr(), n, heads, head_dim, p)
+
+
+def _batch(c, table, lens, cu, n_rows, max_new, max_len, device):
+    if table.dtype != torch.int32 or table.dim() != 2 or table.device != device or \
+            (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be an int32 tensor [n_seqs, pages] on {device} with contiguous rows")
+    seqs, width = table.shape
+    stride = table.stride(0) if seqs > 1 else width
+    if stride < width:
+        raise ValueError("table's rows overlap")
+    if max_len is None:
+        max_len = width * c.page_tokens
+    elif not 0 <= max_len <= width * c.page_tokens:
+        raise ValueError(f"max_len {max_len} exceeds the table's {width} pages of {c.page_tokens} tokens")
+    lens_at = _tensor(lens, "lens", torch.int32, (seqs,), device)
+    cu_at = None
+    if cu is not None:
+        cu_at = _tensor(cu, "cu", torch.int32, (seqs + 1,), device)
+        max_new = n_rows if max_new is None else min(max_new, n_rows)
+        if max_new < 0:
+            raise ValueError("max_new must not be negative")
+    else:
+        if n_rows != seqs:
+            raise ValueError(f"{n_rows} rows for {seqs} sequences: several rows of a sequence need cu")
+        max_new = min(1, n_rows)
+    return N.KV4BatchDesc(table.data_ptr() or None, stride, lens_at, cu_at, seqs, max_len, max_new, n_rows)
+
+
+def _strided(t, name, dtypes, heads, dim, device):
+    """(rows, row stride, head stride) of t [rows, heads, dim]."""
+    if t.dtype not in dtypes or t.dim() != 3 or t.device != device:
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor of {' or '.join(map(str, dtypes))} on {device}")
+    rows, h, d = t.shape
+    if d != dim or (heads is not None and h != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, heads {heads} and head_dim {dim} expected")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    if rows <= 1:
+        s0 = 0
+    if h <= 1:
+        s1 = 0
+    if (s0 | s1) & 7 or t.data_ptr() % (8 * t.element_size()):
+        raise ValueError(f"{name}'s rows and heads must start at multiples of 8 elements")
+    return rows, s0, s1
+
+
+def _check(rc, what):
+    if rc != N.OK:
+        raise N.SplitZipError(rc, what)
+
+
+def _stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _status(status, device):
+    if status is None:
+        return None
+    N._status_word(status)
+    if status.device != device:
+        raise ValueError(f"status must be on {device}")
+    return status.data_ptr()
+
+
+def kv4_append(pages, k, v, table, lens, cu=None, positions=None, mass=None, pos=None, max_new=None, max_len=None,
+               status=None, stream=None) -> None:
+    """Put rows k, v [rows, n_heads, head_dim] (bfloat16, float16 or
+    float8_e5m2, strided views allowed) into their sequences' last slots.
+    ``mass`` of the slots becomes 0 and ``pos`` the rows' ``positions`` (int32
+    [rows]; None: the slot's number)."""
+    device = _pool(pages)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_append(pages, k, v, table, lens, cu, positions, mass, pos, max_new, max_len, status)
+    dim = k.shape[-1] if k.dim() == 3 else 0
+    c = _cache(pages, dim)
+    rows, k0, k1 = _strided(k, "k", _ROWS, c.n_heads, dim, device)
+    rows_v, v0, v1 = _strided(v, "v", (k.dtype,), c.n_heads, dim, device)
+    if rows_v != rows:
+        raise ValueError(f"{rows} rows of k, {rows_v} of v")
+    side = (c.n_pages, c.n_heads, c.page_tokens)
+    b = _batch(c, table, lens, cu, rows, max_new, max_len, device)
+    rc = N.load().splitzip_kv4_append(
+        _byref(c), _byref(b), _ROWS[k.dtype], k.data_ptr() or None, k0, k1, v.data_ptr() or None, v0, v1,
+        _optional(positions, "positions", torch.int32, (rows,), device),
+        _optional(mass, "mass", torch.float32, side, device), _optional(pos, "pos", torch.int32, side, device),
+        _status(status, device), _stream(device))
+    _check(rc, "splitzip_kv4_append")
+
+
+def kv4_read(pages, table, lens, head_dim, cu=None, n_tokens=None, dtype=torch.bfloat16, max_new=None, max_len=None,
+             out=None, status=None, stream=None):
+    """(k, v) [n_tokens, n_heads, head_dim] of the sequences' last slots, the
+    inverse of ``kv4_append``.  ``n_tokens``: packed rows in all (cu[-1]; the
+    number of sequences where cu is None).  ``out``: the two tensors to fill;
+    rows of no sequence are not written."""
+    device = _pool(pages)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_read(pages, table, lens, head_dim, cu, n_tokens, dtype, max_new, max_len, out, status)
+    c = _cache(pages, head_dim)
+    if dtype not in _HALF:
+        raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+    if n_tokens is None:
+        if cu is not None:
+            raise ValueError("n_tokens is needed with cu")
+        n_tokens = table.shape[0]
+    shape = (n_tokens, c.n_heads, head_dim)
+    if out is None:
+        k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
+    else:
+        k, v = out
+        _tensor(k, "out[0]", dtype, shape, device)
+        _tensor(v, "out[1]", dtype, shape, device)
+    b = _batch(c, table, lens, cu, n_tokens, max_new, max_len, device)
+    rc = N.load().splitzip_kv4_read(_byref(c), _byref(b), _HALF[dtype], k.data_ptr() or None, v.data_ptr() or None,
+                                    _status(status, device), _stream(device))
+    _check(rc, "splitzip_kv4_read")
+    return k, v
+
+
+def kv4_attention(q, pages, table, lens, cu=None, max_new=None, scale=None, max_len=None, mass=None, mass_out=None,
+                  return_lse=False, out=None, lse=None, work=None, status=None, stream=None):
+    """Causal attention of packed queries q [rows, n_q_heads, head_dim]
+    (bfloat16 or float16, strided views allowed) over the cache; returns
+    ``out`` (contiguous, q's type), or ``(out, lse)`` with ``return_lse`` or
+    ``lse`` given.  ``scale`` defaults to head_dim ** -0.5.  With ``mass``, the
+    weights that every slot drew are added into ``mass_out`` (default: into
+    ``mass``).  Rows of no sequence are not written."""
+    device = _pool(pages)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_attention(q, pages, table, lens, cu, max_new, scale, max_len, mass, mass_out, return_lse, out,
+                                 lse, work, status)
+    dim = q.shape[-1] if q.dim() == 3 else 0
+    c = _cache(pages, dim)
+    rows, q0, q1 = _strided(q, "q", _HALF, None, dim, device)
+    heads = q.shape[1]
+    b = _batch(c, table, lens, cu, rows, max_new, max_len, device)
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=q.dtype, device=device)
+    else:
+        _tensor(out, "out", q.dtype, (rows, heads, dim), device)
+    if lse is not None:
+        _tensor(lse, "lse", torch.float32, (rows, heads), device)
+    elif return_lse:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
+    mass_at = to = None
+    if mass is not None:
+        side = (c.n_pages, c.n_heads, c.page_tokens)
+        mass_at = to = _tensor(mass, "mass", torch.float32, side, device)
+        if mass_out is not None:
+            to = _tensor(mass_out, "mass_out", torch.float32, side, device)
+    elif mass_out is not None:
+        raise ValueError("mass_out needs mass")
+    lib = N.load()
+    cp, bp = _byref(c), _byref(b)
+    need = lib.splitzip_kv4_attention_work_bytes(cp, bp, heads, mass is not None)
+    if need == 0:
+        raise N.SplitZipError(N.E_INVALID, "splitzip_kv4_attention_work_bytes")
+    if work is None:
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        N._device_buffer(work, "work", need)
+        if work.device != device:
+            raise ValueError(f"work must be on {device}")
+    rc = lib.splitzip_kv4_attention(cp, bp, _HALF[q.dtype], q.data_ptr() or None, q0, q1, heads,
+                                    dim ** -0.5 if scale is None else scale, out.data_ptr() or None,
+                                    None if lse is None else lse.data_ptr() or None, mass_at, to, work.data_ptr(),
+                                    N._nbytes(work), _status(status, device), _stream(device))
+    _check(rc, "splitzip_kv4_attention")
+    return out if lse is None else (out, lse)
+
+
+def kv4_evict(pages, table, lens, mass, pos, next_pos, head_dim, budget, sinks=0, recent=0, max_len=None,
+              lens_out=None, mass_out=None, pos_out=None, work=None, status=None, stream=None):
+    """Cut every sequence longer than ``budget`` slots to the ``budget`` that
+    drew the largest ``mass``, each head for itself; tokens at positions below
+    ``sinks`` or at ``next_pos`` - ``recent`` and beyond always stay.  Returns
+    ``(lens_out, mass_out, pos_out)``, by default the tensors given, updated in
+    place."""
+    device = _pool(pages)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv4_evict(pages, table, lens, mass, pos, next_pos, head_dim, budget, sinks, recent, max_len,
+                             lens_out, mass_out, pos_out, work, status)
+    c = _cache(pages, head_dim)
+    seqs = table.shape[0]
+    side = (c.n_pages, c.n_heads, c.page_tokens)
+    if min(budget, sinks, recent) < 0 or max(budget, sinks, recent) >= 1 << 32:
+        raise ValueError("budget, sinks and recent must be 32-bit counts")
+    lens_out = lens if lens_out is None else lens_out
+    mass_out = mass if mass_out is None else mass_out
+    pos_out = pos if pos_out is None else pos_out
+    b = _batch(c, table, lens, None, seqs, 1, max_len, device)
+    lib = N.load()
+    cp, bp = _byref(c), _byref(b)
+    need = lib.splitzip_kv4_evict_work_bytes(cp, bp, budget)
+    if need == 0:
+        raise N.SplitZipError(N.E_INVALID, "splitzip_kv4_evict_work_bytes")
+    if work is None:
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        N._device_buffer(work, "work", need)
+        if work.device != device:
+            raise ValueError(f"work must be on {device}")
+    rc = lib.splitzip_kv4_evict(
+        cp, bp, budget, sinks, recent, _tensor(next_pos, "next_pos", torch.int32, (seqs,), device),
+        _tensor(mass, "mass", torch.float32, side, device), _tensor(pos, "pos", torch.int32, side, device),
+        _tensor(lens_out, "lens_out", torch.int32, (seqs,), device),
+        _tensor(mass_out, "mass_out", torch.float32, side, device),
+        _tensor(pos_out, "pos_out", torch.int32, side, device), work.data_ptr(), N._nbytes(work),
+        _status(status, device), _stream(device))
+    _check(rc, "splitzip_kv4_evict")
+    return lens_out, mass_out, pos_out
