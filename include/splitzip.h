@@ -418,7 +418,9 @@ size_t splitzip_kv4_attention_work_bytes(const splitzip_kv4_cache* cache, const 
  *              here leave one of their sums in them.
  *   d_work     splitzip_kv4_attention_work_bytes bytes, 256-byte aligned,
  *              overwritten; calls that may overlap need one each.
- * Weights and sums are held in 32 bits.  Only launches kernels, as the codec's
+ * Weights and sums are held in 32 bits; for the product with V a weight counts
+ * with 16 bits, or, in BF16 calls with more than 64 rows (tokens x query heads
+ * of a KV head; 16 where head_dim is 256), as BF16.  Only launches kernels, as the codec's
  * calls.  Returns SPLITZIP_OK, SPLITZIP_E_INVALID, SPLITZIP_E_CAPACITY (d_work
  * too small) or SPLITZIP_E_HIP. */
 int splitzip_kv4_attention(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch, int dtype,

@@ -24,7 +24,19 @@
 
 namespace kv4 {
 
-constexpr int kAttThreads = 256;  // 4 waves, each with key tiles of its own
+constexpr int kAttThreads = 256;  // 4 waves
+
+// Workgroups that the GPU holds at once (256 compute units): the kernel for few
+// rows 3 a unit, by its registers; the one for many 2, by its LDS.
+constexpr uint32_t kFewSlots = 768, kManySlots = 512;
+// Pieces of the weights' sums: nothing to join, so short ones.  768, 1536, 3072
+// in all: 82.5, 81.8, 82.2 us (32 sequences), 60.6, 60.6, 71.8 (24, 35 rows).
+constexpr uint32_t kMassPieces = 1536;
+// Up to so many rows every wave converts the cache for itself, in row tiles of
+// 32 (the second tile's reads are L2's): no barriers and more bytes under way.
+// 64 rows of 128 channels, 16 x 8192 slots: 74 us against 82 through LDS; 128
+// rows: 165 against 132.
+constexpr uint32_t kFewRows = 64;
 
 struct AttArgs {
   Batch a;
@@ -34,15 +46,76 @@ struct AttArgs {
   float* lse;
   const float* mass;
   float* mass_out;
-  float* part_o;    // [seq][head][split][rows_pad][D] unnormalised sums
-  float* part_ml;   // [seq][head][split][rows_pad][2] largest logit (base 2), sum
-  float* row_lse;   // [seq][head][rows_pad] log2 of the sums, for the weights
+  float* part_o;    // [piece][head][rows_max][D] unnormalised sums
+  float* part_ml;   // [piece][head][rows_max][2] largest logit (base 2), sum
+  float* row_lse;   // [seq][head][rows_max] log2 of the sums, for the weights
   uint32_t q_heads, group;
-  uint32_t rows_pad;    // rows (token, head of the group) of the longest sequence, a multiple of 16
-  uint32_t splits;      // of the long axis
-  uint32_t split_len;   // slots each, a multiple of 128
-  float scale2;         // scale * log2 e
+  uint32_t rows_max;  // rows (token, head of the group) of the longest sequence
+  uint32_t pieces;    // wanted in all (Piece); 0: sequences stay whole
+  float scale2;       // scale * log2 e
 };
+
+// The long axis is cut into pieces of one length for all sequences, chosen on
+// the device from the lengths themselves: max_len is only a bound, and with
+// pieces cut from it a ragged batch would leave most workgroups idle.  At least
+// one piece a sequence, a multiple of 128 slots each, at most pieces + n_seqs
+// in all.
+struct Piece {
+  uint32_t seq, index, count;  // of its sequence
+  uint32_t first;              // the sequence's first piece
+  uint32_t len;                // slots of a piece
+  Seq s;
+};
+
+// The piece x (want_seq false), or the pieces of sequence x; every wave finds
+// it for itself.  seq = n_seqs: there is no such piece.
+__device__ inline Piece piece_of(const Batch& a, uint32_t pieces, uint32_t x, bool want_seq) {
+  const uint32_t lane = threadIdx.x & 63;
+  // what a batch of up to 64 sequences is described by, in one round of loads
+  auto at = [&](uint32_t b, int32_t& len, int32_t& row0, int32_t& end) {
+    const bool in = b < a.n_seqs;
+    len = in ? a.lens[b] : 0;
+    row0 = a.cu ? (in ? a.cu[b] : 0) : (int32_t)b;
+    end = a.cu ? (in ? a.cu[b + 1] : 0) : (int32_t)b + 1;
+  };
+  auto checked = [&](int32_t n) { return n < 0 || n > (int32_t)a.max_len ? 0u : (uint32_t)n; };
+  int32_t len0, row00, end0;
+  at(lane, len0, row00, end0);
+  Piece p;
+  p.len = 1u << 30;
+  if (pieces) {
+    uint64_t total = 0;
+    for (uint32_t b = 0; b < a.n_seqs; b += 64) {
+      const uint32_t n = checked(b == 0 ? len0 : b + lane < a.n_seqs ? a.lens[b + lane] : 0);
+      // 64 lengths of up to 2^30 each, summed in two halves
+      total += wave_last(wave_scan(n & 0xFFFFu)) + ((uint64_t)wave_last(wave_scan(n >> 16)) << 16);
+    }
+    p.len = (uint32_t)min((total / pieces + 128) / 128 * 128, (uint64_t)1 << 30);
+  }
+  uint32_t before = 0;
+  for (uint32_t b = 0; b < a.n_seqs; b += 64) {
+    int32_t len = len0, row0 = row00, end = end0;
+    if (b > 0) at(b + lane, len, row0, end);
+    const uint32_t count = b + lane < a.n_seqs ? max(1u, (checked(len) + p.len - 1) / p.len) : 0u;
+    const uint32_t upto = wave_scan(count);
+    const uint64_t hit = __ballot(want_seq ? b + lane == x : before + upto > x);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      p.seq = b + l;
+      p.count = (uint32_t)__builtin_amdgcn_readlane((int)count, l);
+      p.first = before + (uint32_t)__builtin_amdgcn_readlane((int)upto, l) - p.count;
+      p.index = want_seq ? 0 : x - p.first;
+      p.s = seq_from(a, __builtin_amdgcn_readlane(len, l), __builtin_amdgcn_readlane(row0, l),
+                     __builtin_amdgcn_readlane(end, l));
+      return p;
+    }
+    before += wave_last(upto);
+  }
+  p.seq = a.n_seqs;
+  p.index = p.count = p.first = 0;
+  p.s = Seq{0, 0, 0, false};
+  return p;
+}
 
 // Channels of product step m for lane quarter j: an 8-channel run.
 template <int D>
@@ -80,29 +153,33 @@ __device__ inline f32x4 mma(const u32x4 a, const u32x4 b, f32x4 c) {
                                                  0);
 }
 
-// Query rows as the right operand: row r = token * group + head in the group.
+// Query rows as an operand: row r = token * group + head in the group, step m.
 // Rows beyond `rows` are zero.  lo: what BF16 leaves of FP16 values.
+template <int D, bool kHalf>
+__device__ inline void load_q_step(const AttArgs& g, const Seq& s, uint32_t head, uint32_t r, uint32_t rows, uint32_t j,
+                                   uint32_t m, u32x4& hi, u32x4& lo) {
+  const uint32_t tok = r / g.group, hg = r % g.group;
+  const uint8_t* p = g.q + 2 * (((uint64_t)s.row0 + tok) * g.q_row + (uint64_t)(head * g.group + hg) * g.q_head);
+  u32x4 x = {0, 0, 0, 0};
+  if (r < rows) x = *reinterpret_cast<const u32x4*>(p + 2 * chan_of<D>(m, j));
+  if constexpr (kHalf) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = (float)__builtin_bit_cast(_Float16, (uint16_t)x[e]);
+      const float b = (float)__builtin_bit_cast(_Float16, (uint16_t)(x[e] >> 16));
+      hi[e] = pack_bf16(a, b);
+      lo[e] = pack_bf16(a - bf16_lo(hi[e]), b - bf16_hi(hi[e]));
+    }
+  } else {
+    hi = x;
+  }
+}
+
 template <int D, bool kHalf>
 __device__ inline void load_q(const AttArgs& g, const Seq& s, uint32_t head, uint32_t r, uint32_t rows, uint32_t j,
                               u32x4 hi[D / 32], u32x4 lo[D / 32]) {
-  const uint32_t tok = r / g.group, hg = r % g.group;
-  const uint8_t* p = g.q + 2 * (((uint64_t)s.row0 + tok) * g.q_row + (uint64_t)(head * g.group + hg) * g.q_head);
 #pragma unroll
-  for (int m = 0; m < D / 32; ++m) {
-    u32x4 x = {0, 0, 0, 0};
-    if (r < rows) x = *reinterpret_cast<const u32x4*>(p + 2 * chan_of<D>(m, j));
-    if constexpr (kHalf) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = (float)__builtin_bit_cast(_Float16, (uint16_t)x[e]);
-        const float b = (float)__builtin_bit_cast(_Float16, (uint16_t)(x[e] >> 16));
-        hi[m][e] = pack_bf16(a, b);
-        lo[m][e] = pack_bf16(a - bf16_lo(hi[m][e]), b - bf16_hi(hi[m][e]));
-      }
-    } else {
-      hi[m] = x;
-    }
-  }
+  for (int m = 0; m < D / 32; ++m) load_q_step<D, kHalf>(g, s, head, r, rows, j, m, hi[m], lo[m]);
 }
 
 // One lane's share of 16 keys: K codes of its key and quarter, V codes of 4
@@ -113,33 +190,53 @@ struct Raw {
   uint32_t ks, vs;
 };
 
-// Lane (i, j)'s bytes of the 16 slots at `t` (in a page) of `base`.
+// A lane's offsets in the bytes of 16 slots: the same for all, so a load is a
+// scalar base and a constant register.
 template <int D>
-__device__ inline void load_raw(const uint8_t* base, uint32_t shift, uint32_t t, uint32_t i, uint32_t j, Raw<D>& r,
-                                bool want_v = true) {
+struct LaneAt {
   using L = Layout<D>;
-  const uint8_t* k = base + (t + i) * L::kCode;
-  const uint8_t* ks = base + L::k_scales(shift) + (t + i) * L::kScale;
-  const uint8_t* v = base + L::v_codes(shift) + L::v_piece(t + 4 * j, i);
-  const uint8_t* vs = base + L::v_scales(shift) + L::v_scale(t + 4 * j, i * L::kScale / 16);
+  uint32_t k, v, ks, vs;
+  __device__ LaneAt(uint32_t i, uint32_t j)
+      : k(i * L::kCode + j * (D == 64 ? 8 : 16)),
+        v(L::v_piece(4 * j, i)),
+        ks(i * L::kScale + (D == 64 ? j >> 1 : j)),
+        vs(L::v_scale(4 * j, i * L::kScale / 16)) {}
+};
+
+template <bool kOnce, class T>
+__device__ inline T get(const uint8_t* p) {
+  if constexpr (kOnce) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+  return *reinterpret_cast<const T*>(p);
+}
+
+// Lane (i, j)'s bytes of the 16 slots at `t` (in a page, uniform) of `base`.
+// kOnce: no other workgroup reads these codes (non-temporal: 96 -> 87 us on
+// 374 MB of scattered pages); the scales share their lines with other slots'.
+template <int D, bool kOnce, bool kV = true>
+__device__ inline void load_raw(const uint8_t* base, uint32_t shift, uint32_t t, const LaneAt<D>& at, Raw<D>& r) {
+  using L = Layout<D>;
+  const uint8_t* k = base + t * L::kCode;
+  const uint8_t* v = k + L::v_codes(shift);
+  const uint8_t* ks = base + L::k_scales(shift) + t * L::kScale;
+  const uint8_t* vs = base + L::v_scales(shift) + t * L::kScale;
   if constexpr (D == 64) {
-    *reinterpret_cast<u32x2*>(r.k) = *reinterpret_cast<const u32x2*>(k + 8 * j);
-    r.ks = ks[j >> 1];
-    if (want_v) *reinterpret_cast<u32x2*>(r.v) = *reinterpret_cast<const u32x2*>(v);
+    *reinterpret_cast<u32x2*>(r.k) = get<kOnce, u32x2>(k + at.k);
+    r.ks = ks[at.ks];
+    if constexpr (kV) *reinterpret_cast<u32x2*>(r.v) = get<kOnce, u32x2>(v + at.v);
   } else if constexpr (D == 128) {
-    *reinterpret_cast<u32x4*>(r.k) = *reinterpret_cast<const u32x4*>(k + 16 * j);
-    r.ks = ks[j];
-    if (want_v) *reinterpret_cast<u32x4*>(r.v) = *reinterpret_cast<const u32x4*>(v);
+    *reinterpret_cast<u32x4*>(r.k) = get<kOnce, u32x4>(k + at.k);
+    r.ks = ks[at.ks];
+    if constexpr (kV) *reinterpret_cast<u32x4*>(r.v) = get<kOnce, u32x4>(v + at.v);
   } else {
-    *reinterpret_cast<u32x4*>(r.k) = *reinterpret_cast<const u32x4*>(k + 16 * j);
-    *reinterpret_cast<u32x4*>(r.k + 4) = *reinterpret_cast<const u32x4*>(k + 64 + 16 * j);
-    r.ks = ks[j] | (uint32_t)ks[4 + j] << 8;
-    if (want_v) {
-      *reinterpret_cast<u32x4*>(r.v) = *reinterpret_cast<const u32x4*>(v);
-      *reinterpret_cast<u32x4*>(r.v + 4) = *reinterpret_cast<const u32x4*>(v + 16);
+    *reinterpret_cast<u32x4*>(r.k) = get<kOnce, u32x4>(k + at.k);
+    *reinterpret_cast<u32x4*>(r.k + 4) = get<kOnce, u32x4>(k + at.k + 64);
+    r.ks = ks[at.ks] | (uint32_t)ks[at.ks + 4] << 8;
+    if constexpr (kV) {
+      *reinterpret_cast<u32x4*>(r.v) = get<kOnce, u32x4>(v + at.v);
+      *reinterpret_cast<u32x4*>(r.v + 4) = get<kOnce, u32x4>(v + at.v + 16);
     }
   }
-  if (want_v) r.vs = *reinterpret_cast<const uint32_t*>(vs);
+  if constexpr (kV) r.vs = *reinterpret_cast<const uint32_t*>(vs + at.vs);
 }
 
 // Step m's left operand of S^T.
@@ -208,7 +305,7 @@ __device__ inline void clear_v(Raw<D>& r, uint32_t t0, uint32_t end) {
     if (t0 + t >= end) r.vs = (r.vs & ~(0xFFu << (8 * t))) | 127u << (8 * t);
 }
 
-template <int D, int kPair, int kRows, bool kTwo>
+template <int D, int kPair, int kRows>
 __device__ inline void pv_step(const Raw<D>& a, const float sa[4], const Raw<D>& b, const float sb[4],
                                const u32x4 (&p)[kRows], const u32x4 (&pl)[kRows], f32x4 (&o)[kRows][D / 16]) {
   if constexpr (kPair < D / 32) {
@@ -218,12 +315,23 @@ __device__ inline void pv_step(const Raw<D>& a, const float sa[4], const Raw<D>&
     for (int n = 0; n < kRows; ++n) {
       o[n][2 * kPair] = mma(x, p[n], o[n][2 * kPair]);
       o[n][2 * kPair + 1] = mma(y, p[n], o[n][2 * kPair + 1]);
-      if constexpr (kTwo) {
-        o[n][2 * kPair] = mma(x, pl[n], o[n][2 * kPair]);
-        o[n][2 * kPair + 1] = mma(y, pl[n], o[n][2 * kPair + 1]);
-      }
+      o[n][2 * kPair] = mma(x, pl[n], o[n][2 * kPair]);
+      o[n][2 * kPair + 1] = mma(y, pl[n], o[n][2 * kPair + 1]);
     }
-    pv_step<D, kPair + 1, kRows, kTwo>(a, sa, b, sb, p, pl, o);
+    pv_step<D, kPair + 1, kRows>(a, sa, b, sb, p, pl, o);
+  }
+}
+
+// One lane's 4 tokens of V as halves of operands: channel c at to[c][.][lane][.].
+template <int D, int kPair>
+__device__ inline void v_to_lds(const Raw<D>& r, const float s[4], u32x2* to) {
+  if constexpr (kPair < D / 32) {
+    const uint32_t a0 = v_at<D, 0, kPair>(r, s[0]), a1 = v_at<D, 1, kPair>(r, s[1]);
+    const uint32_t a2 = v_at<D, 2, kPair>(r, s[2]), a3 = v_at<D, 3, kPair>(r, s[3]);
+    to[(2 * kPair) * 128] = u32x2{__builtin_amdgcn_perm(a1, a0, 0x05040100), __builtin_amdgcn_perm(a3, a2, 0x05040100)};
+    to[(2 * kPair + 1) * 128] =
+        u32x2{__builtin_amdgcn_perm(a1, a0, 0x07060302), __builtin_amdgcn_perm(a3, a2, 0x07060302)};
+    v_to_lds<D, kPair + 1>(r, s, to);
   }
 }
 
@@ -236,19 +344,22 @@ __device__ inline void store2(uint8_t* out, uint64_t elem, bool half, float a, f
   *reinterpret_cast<uint32_t*>(out + 2 * elem) = w;
 }
 
-// One workgroup: the slots of one split, 16 kRows query rows of one KV head of
+// One workgroup: the slots of one piece, 16 kRows query rows of one KV head of
 // one sequence.  Each wave takes every 4th tile of 32 slots with a softmax of
 // its own; the four are joined through LDS.
 template <int D, int kRows, bool kHalf>
-__global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
+__global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : kRows == 1 || D == 64 ? 3 : 2) void kv4_attend_kernel(AttArgs g) {
   constexpr int kSteps = D / 32;
   __shared__ float sh_o[4][16][D + 4];
   __shared__ float sh_m[4][16 * kRows], sh_l[4][16 * kRows];
   const Batch& a = g.a;
-  const uint32_t split = blockIdx.x, b = blockIdx.z;
-  const uint32_t head = blockIdx.y % a.n_heads, tile = blockIdx.y / a.n_heads;
-  const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, i = lane & 15, j = lane >> 4;
-  const Seq s = seq_of(a, b);
+  const uint32_t head = blockIdx.y, tile = blockIdx.z;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, i = lane & 15, j = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Piece pc = piece_of(a, g.pieces, blockIdx.x, false);
+  const uint32_t b = pc.seq;
+  if (b >= a.n_seqs) return;
+  const Seq s = pc.s;
   if (!s.ok && tid == 0) corrupt(a.status);
   const uint32_t rows = (uint32_t)s.rows * g.group, r0 = tile * 16 * kRows;
   if (r0 >= rows) return;
@@ -256,8 +367,8 @@ __global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
   const int32_t before = s.len - s.rows;
   const int32_t newest = before + (int32_t)(min(r0 + 16 * kRows, rows) - 1) / (int32_t)g.group;
   const uint32_t seen = newest < 0 ? 0u : (uint32_t)newest + 1;  // slots that any row of this tile sees
-  const uint32_t c0 = split * g.split_len, c1 = min(seen, c0 + g.split_len);
-  if (c0 >= c1 && split > 0) return;  // split 0 writes what rows without slots get
+  const uint32_t c0 = pc.index * pc.len, c1 = min(seen, c0 + pc.len);
+  if (c0 >= c1 && c0 > 0) return;  // the first piece writes what rows without slots get
 
   u32x4 qh[kRows][kSteps], ql[kRows][kSteps];
   int32_t lim[kRows];
@@ -273,24 +384,28 @@ __global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) o[n][t] = f32x4{0, 0, 0, 0};
   }
+  // This wave's tiles: 32 slots at first + 128 it.  Lane 2 it + h holds the
+  // page of tile it's half h, for 32 tiles at a time, so that a tile's address
+  // never waits for the block table.
   const uint32_t in_page = (1u << a.page_shift) - 1;
-  auto load_tile = [&](uint32_t at, Raw<D> (&r)[2]) {
+  const uint32_t first = c0 + 32 * wave, n_tiles = first < c1 ? (c1 - first + 127) / 128 : 0;
+  // a half tile wholly behind the end loads the last slots there are instead, unused
+  auto slot_of = [&](uint32_t it, uint32_t h) { return min(first + 128 * it + 16 * h, (c1 - 1) & ~15u); };
+  const LaneAt<D> lane_at(i, j);
+  uint32_t pages = 0;
+  auto load_pages = [&](uint32_t it) {
+    if (n_tiles > 0) pages = page_of(a, b, slot_of(min(it + (lane >> 1), n_tiles - 1), lane & 1) >> a.page_shift);
+  };
+  auto load_tile = [&](uint32_t it, Raw<D> (&r)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      // a half tile wholly behind the end loads the last slots there are instead, unused
-      const uint32_t t = __builtin_amdgcn_readfirstlane(min(at + 16 * h, (c1 - 1) & ~15u));
-      const uint32_t p = page_of(a, b, t >> a.page_shift);
+      const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(2 * (it & 31) + h));
       const uint8_t* base = a.pages + ((uint64_t)p * a.n_heads + head) * a.page_bytes;
-      load_raw<D>(base, a.page_shift, t & in_page, i, j, r[h]);
+      load_raw<D, kRows == 1>(base, a.page_shift, __builtin_amdgcn_readfirstlane(slot_of(it, h)) & in_page, lane_at, r[h]);
     }
   };
-  Raw<D> cur[2], nxt[2];
-  uint32_t at = c0 + 32 * wave;
-  if (at < c1) load_tile(at, nxt);
-  for (; at < c1; at += 128) {
-    cur[0] = nxt[0];
-    cur[1] = nxt[1];
-    if (at + 128 < c1) load_tile(at + 128, nxt);
+  auto compute = [&](uint32_t it, Raw<D> (&cur)[2]) {
+    const uint32_t at = first + 128 * it;
     f32x4 x[kRows][2];
 #pragma unroll
     for (int n = 0; n < kRows; ++n) x[n][0] = x[n][1] = f32x4{0, 0, 0, 0};
@@ -353,7 +468,27 @@ __global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
     float sa[4], sb[4];
     v_scales4(cur[0].vs, sa);
     v_scales4(cur[1].vs, sb);
-    pv_step<D, 0, kRows, true>(cur[0], sa, cur[1], sb, p, pl, o);
+    pv_step<D, 0, kRows>(cur[0], sa, cur[1], sb, p, pl, o);
+  };
+  // Loads run a tile ahead of the products, in two sets of registers.  They
+  // are issued whether or not there is a next tile: behind a branch the wait
+  // for this tile's bytes would be one for the next tile's as well.
+  Raw<D> even[2], odd[2];
+  load_pages(0);
+  auto step = [&](uint32_t it, Raw<D> (&cur)[2], Raw<D> (&nxt)[2]) {
+    const uint32_t ahead = min(it + 1, n_tiles - 1);
+    if (((it + 1) & 31) == 0) load_pages(ahead);
+    load_tile(ahead, nxt);
+    compute(it, cur);
+  };
+  if (n_tiles > 0) {
+    load_tile(0, even);
+    uint32_t it = 0;
+    for (; it + 2 <= n_tiles; it += 2) {
+      step(it, even, odd);
+      step(it + 1, odd, even);
+    }
+    if (it < n_tiles) compute(it, even);
   }
 
   // join the four waves
@@ -366,7 +501,7 @@ __global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
     }
   }
   __syncthreads();
-  const uint32_t row_base = (b * a.n_heads + head) * g.rows_pad;  // fits: checked on the host
+  const uint32_t row_base = (b * a.n_heads + head) * g.rows_max;  // fits: checked on the host
 #pragma unroll
   for (int n = 0; n < kRows; ++n) {
     float top = sh_m[0][16 * n + i];
@@ -388,7 +523,7 @@ __global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
         if (mm[w] != -INFINITY) sum += sh_l[w][16 * n + row] * __builtin_amdgcn_exp2f((mm[w] - all) * g.scale2);
       const uint32_t tok = r / g.group, qh_at = head * g.group + r % g.group;
       const uint64_t out_row = ((uint64_t)s.row0 + tok) * g.q_heads + qh_at;
-      const uint64_t part = ((uint64_t)(b * a.n_heads + head) * g.splits + split) * g.rows_pad + r;
+      const uint64_t part = ((uint64_t)blockIdx.x * a.n_heads + head) * g.rows_max + r;
       const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);  // NaN stays
       for (uint32_t c = 2 * (tid & 15); c < (uint32_t)D; c += 32) {
         float u = 0.0f, v = 0.0f;
@@ -397,7 +532,7 @@ __global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
           u += sh_o[w][row][c];
           v += sh_o[w][row][c + 1];
         }
-        if (g.splits == 1) {
+        if (pc.count == 1) {
           store2(g.out, out_row * D + c, kHalf, u * inv, v * inv);
         } else {
           g.part_o[part * D + c] = u;
@@ -406,7 +541,7 @@ __global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
       }
       if ((tid & 15) == 0) {
         const float top2 = all * g.scale2;
-        if (g.splits == 1) {
+        if (pc.count == 1) {
           const float lse2 = sum == 0.0f ? -INFINITY : top2 + __builtin_amdgcn_logf(sum);
           if (g.lse) g.lse[out_row] = lse2 * 0.69314718055994531f;
           if (g.row_lse) g.row_lse[row_base + r] = lse2;
@@ -420,108 +555,503 @@ __global__ __launch_bounds__(kAttThreads) void kv4_attend_kernel(AttArgs g) {
   }
 }
 
-// Joins the splits: one row (query head of a token) per D / 4 lanes.
+// Query rows of a wave of the kernel for many rows: those of 256 channels fill
+// twice the registers.
+template <int D>
+constexpr int kWaveRows = D == 256 ? 16 : 32;
+
+// Many rows: 128 query rows of one KV head, 32 a wave, over a piece's slots.
+// The four waves convert 64 slots at a time into LDS, 16 slots each, in the
+// order in which the matrix instructions take their operands (a lane's 16
+// bytes side by side: no bank conflicts on either side), and share them: a
+// conversion serves 128 rows.  Two buffers, one barrier a tile; the codes of
+// the tile after the next are on their way meanwhile.  Heads run fastest over
+// the grid, so that one head's row tiles meet in one XCD's L2 (8 heads), and
+// the last rows, which see the most, come first.
 template <int D, bool kHalf>
-__global__ __launch_bounds__(256) void kv4_join_kernel(AttArgs g) {
-  constexpr uint32_t kLanes = D / 4;
+__global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kernel(AttArgs g) {
+  constexpr int kSteps = D / 32, kChans = D / 16, kN = kWaveRows<D> / 16;
+  __shared__ u32x4 sh_k[2][4][kSteps][64];
+  __shared__ u32x2 sh_v[2][2][kChans][64][2];
   const Batch& a = g.a;
-  const uint32_t b = blockIdx.z, head = blockIdx.y;
-  const uint32_t r = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, c = 4 * (threadIdx.x % kLanes);
-  const Seq s = seq_of(a, b);
-  if (r >= (uint32_t)s.rows * g.group) return;
-  const int32_t newest = s.len - s.rows + (int32_t)(r / g.group);
-  const uint32_t seen = newest < 0 ? 0u : (uint32_t)newest + 1;
-  const uint32_t n = max(1u, (seen + g.split_len - 1) / g.split_len);  // splits with slots of this row
-  const uint64_t first = (uint64_t)(b * a.n_heads + head) * g.splits * g.rows_pad + r;
-  float top = -INFINITY;
-  for (uint32_t k = 0; k < n; ++k) top = fmaxf(top, g.part_ml[2 * (first + (uint64_t)k * g.rows_pad)]);
-  float sum = 0.0f;
-  f32x4 o = {0, 0, 0, 0};
-  for (uint32_t k = 0; k < n; ++k) {
-    const uint64_t at = first + (uint64_t)k * g.rows_pad;
-    const float mk = g.part_ml[2 * at];
-    if (mk == -INFINITY) continue;
-    const float f = __builtin_amdgcn_exp2f(mk - top);
-    sum += g.part_ml[2 * at + 1] * f;
-    o += *reinterpret_cast<const f32x4*>(g.part_o + at * D + c) * f;
+  const uint32_t head = blockIdx.x, tile = gridDim.y - 1 - blockIdx.y;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, i = lane & 15, j = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Piece pc = piece_of(a, g.pieces, blockIdx.z, false);
+  const uint32_t b = pc.seq;
+  if (b >= a.n_seqs) return;
+  const Seq s = pc.s;
+  if (!s.ok && tid == 0) corrupt(a.status);
+  const uint32_t rows = (uint32_t)s.rows * g.group, r0 = tile * 4 * kWaveRows<D>;
+  if (r0 >= rows) return;
+  const int32_t before = s.len - s.rows;
+  auto seen_by = [&](uint32_t r) -> uint32_t {  // slots that row r sees
+    const int32_t n = before + (int32_t)(min(r, rows - 1) / g.group) + 1;
+    return n < 0 ? 0u : (uint32_t)n;
+  };
+  const uint32_t seen = seen_by(r0 + 4 * kWaveRows<D> - 1);
+  const uint32_t c0 = pc.index * pc.len, c1 = min(seen, c0 + pc.len);
+  if (c0 >= c1 && c0 > 0) return;  // the first piece writes what rows without slots get
+  const uint32_t w0 = r0 + kWaveRows<D> * wave;  // this wave's rows
+  const uint32_t w_first = seen_by(w0), w_last = w0 < rows ? seen_by(w0 + kWaveRows<D> - 1) : 0;
+
+  u32x4 qh[kN][kSteps], ql[kN][kSteps];
+  int32_t lim[kN];
+  f32x4 o[kN][kChans];
+  float m[kN], l[kN];
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    const uint32_t r = w0 + 16 * n + i;
+    load_q<D, kHalf>(g, s, head, r, rows, j, qh[n], ql[n]);
+    lim[n] = before + (int32_t)(r / g.group) + 1;
+    m[n] = -INFINITY;
+    l[n] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kChans; ++t) o[n][t] = f32x4{0, 0, 0, 0};
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-  const uint64_t out_row = ((uint64_t)s.row0 + r / g.group) * g.q_heads + head * g.group + r % g.group;
-  store2(g.out, out_row * D + c, kHalf, o[0] * inv, o[1] * inv);
-  store2(g.out, out_row * D + c + 2, kHalf, o[2] * inv, o[3] * inv);
-  if (c == 0) {
-    const float lse2 = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum);
-    if (g.lse) g.lse[out_row] = lse2 * 0.69314718055994531f;
-    if (g.row_lse) g.row_lse[(b * a.n_heads + head) * g.rows_pad + r] = lse2;
+  // this wave's 16 slots of a tile; lane t holds the page of tile t, 64 tiles at a time
+  const uint32_t in_page = (1u << a.page_shift) - 1, n_tiles = c1 > c0 ? (c1 - c0 + 63) / 64 : 0;
+  const LaneAt<D> lane_at(i, j);
+  auto slot_of = [&](uint32_t t) { return min(c0 + 64 * t + 16 * wave, (c1 - 1) & ~15u); };
+  uint32_t pages = 0;
+  auto load_pages = [&](uint32_t t) { pages = page_of(a, b, slot_of(min(t + lane, n_tiles - 1)) >> a.page_shift); };
+  Raw<D> raw;
+  auto load_tile = [&](uint32_t t) {
+    const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(t & 63));
+    load_raw<D, false>(a.pages + ((uint64_t)p * a.n_heads + head) * a.page_bytes, a.page_shift,
+                       __builtin_amdgcn_readfirstlane(slot_of(t)) & in_page, lane_at, raw);
+  };
+  auto convert = [&](uint32_t t) {  // raw -> LDS
+    const uint32_t at = c0 + 64 * t + 16 * wave, buf = t & 1;
+    if (at + 16 > c1) clear_v<D>(raw, at + 4 * j, c1);
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) sh_k[buf][wave][st][lane] = k_operand<D>(raw, st);
+    float sv[4];
+    v_scales4(raw.vs, sv);
+    v_to_lds<D, 0>(raw, sv, &sh_v[buf][wave >> 1][0][lane][wave & 1]);
+  };
+  if (n_tiles > 0) {
+    load_pages(0);
+    load_tile(0);
+    convert(0);
+    load_tile(min(1u, n_tiles - 1));
+  }
+  for (uint32_t t = 0; t < n_tiles; ++t) {
+    __syncthreads();
+    const uint32_t at = c0 + 64 * t, buf = t & 1;
+    if (at < w_last) {
+      f32x4 x[kN][4];
+#pragma unroll
+      for (int kt = 0; kt < 4; ++kt) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) x[n][kt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+          const u32x4 k = sh_k[buf][kt][st][lane];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            x[n][kt] = mma(k, qh[n][st], x[n][kt]);
+            if constexpr (kHalf) x[n][kt] = mma(k, ql[n][st], x[n][kt]);
+          }
+        }
+      }
+      if (at + 64 > w_first) {  // some row does not see all of the tile
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((int32_t)(at + 16 * kt + 4 * j + e) >= lim[n]) x[n][kt][e] = -INFINITY;
+      }
+      u32x4 p[kN][2], pl[kN][2];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        float top = m[n];
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, x[n][kt][e]);
+        top = max_quarters(top);
+        if (__any(top > m[n])) {
+          const float f = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[n] - top) * g.scale2);
+          m[n] = top;
+          l[n] *= f;
+#pragma unroll
+          for (int c = 0; c < kChans; ++c) o[n][c] *= f;
+        }
+        const float shift = m[n] == -INFINITY ? 0.0f : m[n] * g.scale2;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float w0_ = __builtin_amdgcn_exp2f(fmaf(x[n][kt][2 * h], g.scale2, -shift));
+            const float w1_ = __builtin_amdgcn_exp2f(fmaf(x[n][kt][2 * h + 1], g.scale2, -shift));
+            l[n] += w0_ + w1_;
+            const uint32_t hi = pack_bf16(w0_, w1_);
+            p[n][kt >> 1][2 * (kt & 1) + h] = hi;
+            // FP16 results need more of the weights than BF16 holds
+            if constexpr (kHalf) pl[n][kt >> 1][2 * (kt & 1) + h] = pack_bf16(w0_ - bf16_lo(hi), w1_ - bf16_hi(hi));
+          }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < kChans; ++c) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(&sh_v[buf][h][c][lane][0]);
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            o[n][c] = mma(v, p[n][h], o[n][c]);
+            if constexpr (kHalf) o[n][c] = mma(v, pl[n][h], o[n][c]);
+          }
+        }
+    }
+    if (t + 1 < n_tiles) {
+      convert(t + 1);
+      const uint32_t ahead = min(t + 2, n_tiles - 1);
+      if (((t + 2) & 63) == 0) load_pages(ahead);
+      load_tile(ahead);
+    }
+  }
+  // lane (i, j) holds channels (4j + e) D/16 .. of row i
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+    l[n] = sum_quarters(l[n]);
+    const uint32_t r = w0 + 16 * n + i;
+    if (r >= rows) continue;
+    const uint64_t out_row = ((uint64_t)s.row0 + r / g.group) * g.q_heads + head * g.group + r % g.group;
+    const uint64_t part = ((uint64_t)blockIdx.z * a.n_heads + head) * g.rows_max + r;
+    const float sum = l[n], inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t c = (4 * j + e) * kChans;
+      if (pc.count == 1) {
+#pragma unroll
+        for (int t = 0; t < kChans; t += 2)
+          store2(g.out, out_row * D + c + t, kHalf, o[n][t][e] * inv, o[n][t + 1][e] * inv);
+      } else {
+#pragma unroll
+        for (int t = 0; t < kChans; t += 4)
+          *reinterpret_cast<f32x4*>(g.part_o + part * D + c + t) =
+              f32x4{o[n][t][e], o[n][t + 1][e], o[n][t + 2][e], o[n][t + 3][e]};
+      }
+    }
+    if (j == 0) {
+      const float top2 = m[n] * g.scale2;
+      if (pc.count == 1) {
+        const float lse2 = sum == 0.0f ? -INFINITY : top2 + __builtin_amdgcn_logf(sum);
+        if (g.lse) g.lse[out_row] = lse2 * 0.69314718055994531f;
+        if (g.row_lse) g.row_lse[(b * a.n_heads + head) * g.rows_max + r] = lse2;
+      } else {
+        g.part_ml[2 * part] = top2;
+        g.part_ml[2 * part + 1] = sum;
+      }
+    }
   }
 }
 
-// Adds the weights that each slot drew: the logits again (K is half of the
-// cache), p = 2^(x - lse) and its sum over the rows, in a fixed order.  A wave
-// has 32 slots.
-template <int D, bool kHalf>
-__global__ __launch_bounds__(kAttThreads) void kv4_mass_kernel(AttArgs g) {
+// Joins the pieces: D / 4 lanes hold a row's channels.  kSpread (few rows): the
+// workgroup's lane groups share one row's pieces and are joined through LDS;
+// else every group has a row of its own.
+template <int D, bool kHalf, bool kSpread>
+__global__ __launch_bounds__(256) void kv4_join_kernel(AttArgs g) {
+  constexpr uint32_t kLanes = D / 4, kGroups = 256 / kLanes, kAhead = 4;
+  __shared__ f32x4 sh_o[kSpread ? kGroups : 1][kLanes];
+  __shared__ float sh_m[kGroups], sh_l[kGroups];
+  const Batch& a = g.a;
+  const uint32_t head = blockIdx.y;
+  const uint32_t lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const Piece pc = piece_of(a, g.pieces, blockIdx.z, true);
+  if (pc.count == 1) return;  // written by the attention itself
+  const Seq s = pc.s;
+  const uint32_t r = kSpread ? blockIdx.x : blockIdx.x * kGroups + group, rows = (uint32_t)s.rows * g.group;
+  if (kSpread ? r >= rows : blockIdx.x * kGroups >= rows) return;
+  const int32_t newest = s.len - s.rows + (int32_t)(r / g.group);
+  const uint32_t seen = newest < 0 ? 0u : (uint32_t)newest + 1;
+  // pieces with slots of this row
+  const uint32_t n = r < rows ? max(1u, (seen + pc.len - 1) / pc.len) : 0;
+  const uint32_t begin = kSpread ? group : 0, step = kSpread ? kGroups : 1;
+  const uint64_t first = ((uint64_t)pc.first * a.n_heads + head) * g.rows_max + r, next = (uint64_t)a.n_heads * g.rows_max;
+  float top = -INFINITY, sum = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  for (uint32_t k = begin; k < n; k += kAhead * step) {
+    float mk[kAhead], lk[kAhead];
+    f32x4 ok[kAhead];
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u) {  // the loads of a round are under way together
+      const uint64_t at = first + (uint64_t)min(k + u * step, n - 1) * next;
+      mk[u] = k + u * step < n ? g.part_ml[2 * at] : -INFINITY;
+      lk[u] = g.part_ml[2 * at + 1];
+      ok[u] = *reinterpret_cast<const f32x4*>(g.part_o + at * D + 4 * lane);
+    }
+    float now = top;
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u) now = fmaxf(now, mk[u]);
+    if (now == -INFINITY) continue;
+    const float f = __builtin_amdgcn_exp2f(top - now);
+    top = now;
+    sum *= f;
+    o *= f;
+#pragma unroll
+    for (uint32_t u = 0; u < kAhead; ++u) {
+      const float fk = __builtin_amdgcn_exp2f(mk[u] - now);  // 0 for a piece without slots of the row
+      sum += lk[u] * fk;
+      o += ok[u] * fk;
+    }
+  }
+  if constexpr (kSpread) {
+    sh_o[group][lane] = o;
+    if (lane == 0) {
+      sh_m[group] = top;
+      sh_l[group] = sum;
+    }
+    __syncthreads();
+    if (group != 0) return;
+    for (uint32_t k = 1; k < kGroups; ++k) top = fmaxf(top, sh_m[k]);
+    sum = 0.0f;
+    o = f32x4{0, 0, 0, 0};
+    for (uint32_t k = 0; k < kGroups; ++k) {
+      if (sh_m[k] == -INFINITY) continue;
+      const float f = __builtin_amdgcn_exp2f(sh_m[k] - top);
+      sum += sh_l[k] * f;
+      o += sh_o[k][lane] * f;
+    }
+  }
+  if (r >= rows) return;
+  const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+  const uint64_t out_row = ((uint64_t)s.row0 + r / g.group) * g.q_heads + head * g.group + r % g.group;
+  store2(g.out, out_row * D + 4 * lane, kHalf, o[0] * inv, o[1] * inv);
+  store2(g.out, out_row * D + 4 * lane + 2, kHalf, o[2] * inv, o[3] * inv);
+  if (lane == 0) {
+    const float lse2 = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum);
+    if (g.lse) g.lse[out_row] = lse2 * 0.69314718055994531f;
+    if (g.row_lse) g.row_lse[(pc.seq * a.n_heads + head) * g.rows_max + r] = lse2;
+  }
+}
+
+// The weights that the slots drew: the logits again (K is half of the cache,
+// and keeping them would cost 4 bytes for each of its rows), p = 2^(x - lse) and
+// its sum over the rows in a fixed order.  Here the products are S = Q K^T, so
+// that a lane has one key and four rows: two exchanges sum a key's column.
+//
+// Few rows: Q stays in registers, a wave takes 64 slots at a time.
+template <int D, int kRows, bool kHalf>
+__global__ __launch_bounds__(kAttThreads, 2) void kv4_mass_kernel(AttArgs g) {
   constexpr int kSteps = D / 32;
   const Batch& a = g.a;
-  const uint32_t b = blockIdx.z, head = blockIdx.y;
-  const uint32_t tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, i = lane & 15, j = lane >> 4;
+  const uint32_t head = blockIdx.y;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, i = lane & 15, j = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Piece pc = piece_of(a, g.pieces, blockIdx.x, false);
+  const uint32_t b = pc.seq;
+  if (b >= a.n_seqs) return;
+  const Seq s = pc.s;
+  if (!s.ok) return;
+  const uint32_t c0 = pc.index * pc.len, c1 = min((uint32_t)s.len, c0 + pc.len);
+  const uint32_t first = c0 + 64 * wave;
+  if (first >= c1) return;
+  const uint32_t n_tiles = (c1 - first + 255) / 256;
+  const uint32_t rows = (uint32_t)s.rows * g.group;
+  const int32_t before = s.len - s.rows;
+  u32x4 qh[kRows][kSteps], ql[kRows][kSteps];
+  float lse2[kRows][4];
+  int32_t lim[kRows][4];
+#pragma unroll
+  for (int n = 0; n < kRows; ++n) {
+    load_q<D, kHalf>(g, s, head, 16 * n + i, rows, j, qh[n], ql[n]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t r = 16 * n + 4 * j + e;
+      lse2[n][e] = r < rows ? g.row_lse[(b * a.n_heads + head) * g.rows_max + r] : INFINITY;
+      lim[n][e] = r < rows ? before + (int32_t)(r / g.group) + 1 : 0;
+    }
+  }
+  const uint32_t in_page = (1u << a.page_shift) - 1;
+  const LaneAt<D> lane_at(i, j);
+  // lane 4 t + h holds the page of tile t's quarter h, for 16 tiles at a time
+  auto slot_of = [&](uint32_t t, uint32_t h) { return min(first + 256 * t + 16 * h, (c1 - 1) & ~15u); };
+  uint32_t pages = 0;
+  auto load_pages = [&](uint32_t t) { pages = page_of(a, b, slot_of(min(t + (lane >> 2), n_tiles - 1), lane & 3) >> a.page_shift); };
+  auto page_at = [&](uint32_t t, uint32_t h) { return (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(4 * (t & 15) + h)); };
+  auto load_tile = [&](uint32_t t, Raw<D> (&r)[4]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      load_raw<D, true, false>(a.pages + ((uint64_t)page_at(t, h) * a.n_heads + head) * a.page_bytes, a.page_shift,
+                               __builtin_amdgcn_readfirstlane(slot_of(t, h)) & in_page, lane_at, r[h]);
+  };
+  // this lane's slot of a tile, as an index of the mass arrays
+  auto own_at = [&](uint32_t t) {
+    const uint32_t p = j == 0 ? page_at(t, 0) : j == 1 ? page_at(t, 1) : j == 2 ? page_at(t, 2) : page_at(t, 3);
+    return (((uint64_t)p * a.n_heads + head) << a.page_shift) + ((first + 256 * t + lane) & in_page);
+  };
+  auto compute = [&](uint32_t t, Raw<D> (&r)[4], uint64_t to, float old) {
+    const uint32_t at = first + 256 * t;
+    float own = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      f32x4 x[kRows];
+#pragma unroll
+      for (int n = 0; n < kRows; ++n) x[n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const u32x4 k = k_operand<D>(r[h], st);
+#pragma unroll
+        for (int n = 0; n < kRows; ++n) {
+          x[n] = mma(qh[n][st], k, x[n]);
+          if constexpr (kHalf) x[n] = mma(ql[n][st], k, x[n]);
+        }
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < kRows; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = __builtin_amdgcn_exp2f(fmaf(x[n][e], g.scale2, -lse2[n][e]));
+          sum += (int32_t)(at + 16 * h + i) < lim[n][e] ? w : 0.0f;
+        }
+      sum = sum_quarters(sum);
+      own = (uint32_t)h == j ? sum : own;
+    }
+    if (at + lane < c1) g.mass_out[to] = old + own;
+  };
+  Raw<D> even[4], odd[4];
+  auto step = [&](uint32_t t, Raw<D> (&cur)[4], Raw<D> (&nxt)[4]) {
+    const uint64_t to = own_at(t);
+    const float old = first + 256 * t + lane < c1 ? g.mass[to] : 0.0f;
+    const uint32_t ahead = min(t + 1, n_tiles - 1);
+    if (((t + 1) & 15) == 0) load_pages(ahead);
+    load_tile(ahead, nxt);
+    compute(t, cur, to, old);
+  };
+  load_pages(0);
+  load_tile(0, even);
+  for (uint32_t t = 0; t < n_tiles; t += 2) {
+    step(t, even, odd);
+    if (t + 1 < n_tiles) step(t + 1, odd, even);
+  }
+}
+
+// Many rows: 64 slots a wave stay in registers as operands, the query rows come
+// through LDS, 32 at a time for the four waves' 256 slots.
+template <int D, bool kHalf>
+__global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_mass_rows_kernel(AttArgs g) {
+  constexpr int kSteps = D / 32, kTerms = kHalf ? 2 : 1, kMine = 2 * kSteps / 4;  // operands that a wave stages
+  __shared__ u32x4 sh_q[2][kTerms][2 * kSteps][64];
+  __shared__ float sh_lse[2][32];
+  const Batch& a = g.a;
+  const uint32_t head = blockIdx.x, b = blockIdx.z;
+  const uint32_t tid = threadIdx.x, lane = tid & 63, i = lane & 15, j = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Seq s = seq_of(a, b);
   if (!s.ok) return;
-  const uint32_t at = (blockIdx.x * 4 + wave) * 32, len = (uint32_t)s.len;
-  if (at >= len) return;
+  const uint32_t w_at = blockIdx.y * 256, at = w_at + 64 * wave, len = (uint32_t)s.len;
+  if (w_at >= len) return;
   const uint32_t rows = (uint32_t)s.rows * g.group;
   const int32_t before = s.len - s.rows;
   const uint32_t in_page = (1u << a.page_shift) - 1;
-  Raw<D> raw[2];
-  uint32_t page[2];
+  const LaneAt<D> lane_at(i, j);
+  u32x4 k[4][kSteps];
+  uint32_t page[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 4; ++h) {
     const uint32_t t = __builtin_amdgcn_readfirstlane(min(at + 16 * h, (len - 1) & ~15u));
     page[h] = page_of(a, b, t >> a.page_shift);
-    load_raw<D>(a.pages + ((uint64_t)page[h] * a.n_heads + head) * a.page_bytes, a.page_shift, t & in_page, i, j,
-                raw[h], false);
-  }
-  float add[2][4] = {};
-  for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
-    if (before + (int32_t)(min(r0 + 16, rows) - 1) / (int32_t)g.group < (int32_t)at) continue;  // rows before these slots
-    u32x4 qh[kSteps], ql[kSteps];
-    const uint32_t r = r0 + i;
-    load_q<D, kHalf>(g, s, head, r, rows, j, qh, ql);
-    const int32_t lim = before + (int32_t)(r / g.group) + 1;
-    const float lse2 = r < rows ? g.row_lse[(b * a.n_heads + head) * g.rows_pad + r] : INFINITY;
+    Raw<D> raw;
+    load_raw<D, true, false>(a.pages + ((uint64_t)page[h] * a.n_heads + head) * a.page_bytes, a.page_shift, t & in_page,
+                             lane_at, raw);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      f32x4 x = {0, 0, 0, 0};
+    for (int st = 0; st < kSteps; ++st) k[h][st] = k_operand<D>(raw, st);
+  }
+  // the first rows that see any of the workgroup's slots
+  const int32_t tok0 = (int32_t)w_at - before;
+  const uint32_t begin = tok0 > 0 ? (uint32_t)tok0 * g.group / 32 * 32 : 0;
+  u32x4 mh[kMine], ml[kMine];
+  float m_lse = 0.0f;
+  auto fetch = [&](uint32_t r0) {  // rows r0 .. r0 + 31: global -> registers
+#pragma unroll
+    for (int f = 0; f < kMine; ++f) {
+      const uint32_t id = wave + 4 * f, r = r0 + 16 * (id / kSteps) + i;
+      load_q_step<D, kHalf>(g, s, head, r, rows, j, id % kSteps, mh[f], ml[f]);
+    }
+    if (tid < 32) {
+      m_lse = r0 + tid < rows ? g.row_lse[(b * a.n_heads + head) * g.rows_max + r0 + tid] : INFINITY;
+      if (m_lse == -INFINITY) m_lse = INFINITY;  // a row without slots adds nothing
+    }
+  };
+  auto put = [&](uint32_t buf) {
+#pragma unroll
+    for (int f = 0; f < kMine; ++f) {
+      sh_q[buf][0][wave + 4 * f][lane] = mh[f];
+      if constexpr (kHalf) sh_q[buf][1][wave + 4 * f][lane] = ml[f];
+    }
+    if (tid < 32) sh_lse[buf][tid] = m_lse;
+  };
+  float sum[4] = {};
+  if (begin < rows) {
+    fetch(begin);
+    put(0);
+  }
+  uint32_t buf = 0;
+  for (uint32_t r0 = begin; r0 < rows; r0 += 32, buf ^= 1) {
+    __syncthreads();
+    if (r0 + 32 < rows) fetch(r0 + 32);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const uint32_t ra = r0 + 16 * n;
+      if (ra >= rows) continue;
+      const int32_t seen = before + (int32_t)(ra / g.group) + 1;                            // by the first row
+      const int32_t most = before + (int32_t)(min(ra + 16, rows) - 1) / (int32_t)g.group + 1;  // and the last
+      if (most <= (int32_t)at) continue;
+      f32x4 x[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) x[h] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int st = 0; st < kSteps; ++st) {
-        const u32x4 k = k_operand<D>(raw[h], st);
-        x = mma(k, qh[st], x);
-        if constexpr (kHalf) x = mma(k, ql[st], x);
+        const u32x4 q = sh_q[buf][0][n * kSteps + st][lane];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) x[h] = mma(q, k[h][st], x[h]);
+        if constexpr (kHalf) {
+          const u32x4 ql = sh_q[buf][1][n * kSteps + st][lane];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) x[h] = mma(ql, k[h][st], x[h]);
+        }
+      }
+      const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&sh_lse[buf][16 * n + 4 * j]);
+      if (seen < (int32_t)at + 64) {  // some row does not see all of the slots
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t lim = before + (int32_t)((ra + 4 * j + e) / g.group) + 1;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if ((int32_t)(at + 16 * h + i) >= lim || ra + 4 * j + e >= rows) x[h][e] = -INFINITY;
+        }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (r < rows && (int32_t)(at + 16 * h + 4 * j + e) < lim)
-          add[h][e] += __builtin_amdgcn_exp2f(fmaf(x[e], g.scale2, -lse2));
+      for (int h = 0; h < 4; ++h) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_exp2f(fmaf(x[h][e], g.scale2, -lse2[e]));
+        sum[h] += (w[0] + w[1]) + (w[2] + w[3]);
+      }
     }
+    if (r0 + 32 < rows) put(buf ^ 1);
   }
+  float own = 0.0f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v = add[h][e];
-#pragma unroll
-      for (int k = 1; k < 16; k *= 2) v += __shfl_xor(v, k, 64);
-      const uint32_t slot = at + 16 * h + 4 * j + e;
-      if (i == 0 && slot < len) {
-        const uint64_t to = (((uint64_t)page[h] * a.n_heads + head) << a.page_shift) + (slot & in_page);
-        g.mass_out[to] = g.mass[to] + v;
-      }
-    }
+  for (int h = 0; h < 4; ++h) {
+    const float v = sum_quarters(sum[h]);
+    own = (uint32_t)h == j ? v : own;
+  }
+  if (at + lane < len) {
+    const uint32_t p = j == 0 ? page[0] : j == 1 ? page[1] : j == 2 ? page[2] : page[3];
+    const uint64_t to = (((uint64_t)p * a.n_heads + head) << a.page_shift) + ((at + lane) & in_page);
+    g.mass_out[to] = g.mass[to] + own;
+  }
 }
 
-// How a call is cut: rows per workgroup, splits of the long axis.
+// How a call is cut: rows per workgroup, pieces of the long axis.
 struct Plan {
-  uint32_t group, rows_pad, row_tiles, tile_rows, splits, split_len;
+  uint32_t group, rows_max, row_tiles, tile_rows, pieces, grid;
   uint64_t part_o, part_ml, row_lse, bytes;  // offsets in the work area
 };
 
@@ -529,19 +1059,21 @@ inline bool plan_of(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, ui
   if (q_heads == 0 || q_heads % c->n_heads || q_heads / c->n_heads > kMaxGroup) return false;
   p->group = q_heads / c->n_heads;
   const uint64_t rows = (uint64_t)b->max_new * p->group;
-  p->tile_rows = rows <= 16 || c->head_dim == 256 ? 16 : 32;  // 32 rows of 256 channels do not fit the registers
-  p->rows_pad = (uint32_t)up(rows, 64);
-  p->row_tiles = (uint32_t)(up(rows, p->tile_rows) / p->tile_rows);
-  const uint64_t heads = (uint64_t)b->n_seqs * c->n_heads;
-  // about 1024 workgroups (4 on each compute unit), 128 slots or more each
-  const uint64_t total = heads * p->row_tiles * b->max_len;
-  uint64_t len = up(total / 1024 + 1, 128);
-  if (len > b->max_len) len = up(b->max_len ? b->max_len : 1, 128);
-  p->split_len = (uint32_t)len;
-  p->splits = (uint32_t)((b->max_len + len - 1) / len);
-  if (p->splits == 0) p->splits = 1;
-  const uint64_t n = heads * p->rows_pad, parts = p->splits > 1 ? n * p->splits : 0;
-  if (n >= (1ull << 32) || (uint64_t)p->row_tiles * c->n_heads > 65535) return false;
+  // rows of a workgroup: few rows have the cache converted by every wave for itself, many share it through LDS
+  p->tile_rows = rows <= 16 ? 16 : c->head_dim == 256 ? 64 : rows <= kFewRows ? 32 : 128;
+  const uint64_t tiles = up(rows, p->tile_rows) / p->tile_rows, n = (uint64_t)b->n_seqs * c->n_heads * rows;
+  if (tiles > 65535 || n >= (1ull << 32)) return false;
+  p->rows_max = (uint32_t)rows;
+  p->row_tiles = (uint32_t)tiles;
+  const uint64_t across = (uint64_t)c->n_heads * (tiles ? tiles : 1);
+  const uint64_t round = (p->tile_rows >= 64 ? kManySlots : kFewSlots) / across;
+  uint64_t pieces = round >= 4ull * b->n_seqs ? round - b->n_seqs : 2 * round;
+  if (pieces < b->n_seqs) pieces = round ? b->n_seqs : 0;  // 0: enough rows to fill the GPU, no cut
+  // pieces are 128 slots or more
+  const uint64_t most = (uint64_t)b->n_seqs * (up(b->max_len ? b->max_len : 1, 128) / 128);
+  p->grid = (uint32_t)(pieces + b->n_seqs < most ? pieces + b->n_seqs : most);
+  p->pieces = (uint32_t)pieces;
+  const uint64_t parts = p->grid > b->n_seqs ? (uint64_t)p->grid * c->n_heads * rows : 0;
   p->part_o = 0;
   p->part_ml = up(parts * c->head_dim * 4, 256);
   p->row_lse = p->part_ml + up(parts * 8, 256);
@@ -552,20 +1084,43 @@ inline bool plan_of(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, ui
 
 template <int D, bool kHalf>
 int attend(const Plan& p, const splitzip_kv4_batch* b, const AttArgs& g, hipStream_t stream) {
-  const dim3 grid(p.splits, p.row_tiles * g.a.n_heads, g.a.n_seqs);
+  const dim3 grid(p.grid, g.a.n_heads, p.row_tiles);
+  if (p.tile_rows >= 64) kv4_extend_kernel<D, kHalf><<<dim3(g.a.n_heads, p.row_tiles, p.grid), kAttThreads, 0, stream>>>(g);
   if constexpr (D != 256) {
     if (p.tile_rows == 32) kv4_attend_kernel<D, 2, kHalf><<<grid, kAttThreads, 0, stream>>>(g);
   }
   if (p.tile_rows == 16) kv4_attend_kernel<D, 1, kHalf><<<grid, kAttThreads, 0, stream>>>(g);
   if (hipGetLastError() != hipSuccess) return SPLITZIP_E_HIP;
-  if (p.splits > 1) {
-    const uint32_t per = 256 / (D / 4);
-    kv4_join_kernel<D, kHalf>
-        <<<dim3((b->max_new * p.group + per - 1) / per, g.a.n_heads, g.a.n_seqs), 256, 0, stream>>>(g);
+  if (p.grid > b->n_seqs) {
+    // a workgroup a row until those fill the GPU
+    if ((uint64_t)p.rows_max * g.a.n_heads * g.a.n_seqs <= 2048) {
+      kv4_join_kernel<D, kHalf, true><<<dim3(p.rows_max, g.a.n_heads, g.a.n_seqs), 256, 0, stream>>>(g);
+    } else {
+      const uint32_t per = 1024 / D;
+      kv4_join_kernel<D, kHalf, false>
+          <<<dim3((p.rows_max + per - 1) / per, g.a.n_heads, g.a.n_seqs), 256, 0, stream>>>(g);
+    }
     if (hipGetLastError() != hipSuccess) return SPLITZIP_E_HIP;
   }
   if (g.mass_out && b->max_len > 0) {
-    kv4_mass_kernel<D, kHalf><<<dim3((b->max_len + 127) / 128, g.a.n_heads, g.a.n_seqs), kAttThreads, 0, stream>>>(g);
+    const uint32_t rows = p.rows_max;
+    if (rows <= (D == 256 ? 16 : 64)) {
+      // pieces of their own: no results to join, so short ones, about 6 workgroups a compute unit
+      AttArgs m = g;
+      const uint64_t most = (uint64_t)b->n_seqs * ((b->max_len + 127) / 128);
+      uint64_t pieces = kMassPieces / g.a.n_heads + 1;
+      if (pieces < b->n_seqs) pieces = b->n_seqs;
+      m.pieces = (uint32_t)pieces;
+      const dim3 grid((uint32_t)(pieces + b->n_seqs < most ? pieces + b->n_seqs : most), g.a.n_heads);
+      if (rows <= 16) kv4_mass_kernel<D, 1, kHalf><<<grid, kAttThreads, 0, stream>>>(m);
+      if constexpr (D != 256) {
+        if (rows > 32) kv4_mass_kernel<D, 4, kHalf><<<grid, kAttThreads, 0, stream>>>(m);
+        else if (rows > 16) kv4_mass_kernel<D, 2, kHalf><<<grid, kAttThreads, 0, stream>>>(m);
+      }
+    } else {
+      kv4_mass_rows_kernel<D, kHalf>
+          <<<dim3(g.a.n_heads, (b->max_len + 255) / 256, g.a.n_seqs), kAttThreads, 0, stream>>>(g);
+    }
     if (hipGetLastError() != hipSuccess) return SPLITZIP_E_HIP;
   }
   return SPLITZIP_OK;
@@ -615,9 +1170,8 @@ int splitzip_kv4_attention(const splitzip_kv4_cache* cache, const splitzip_kv4_b
   g.row_lse = d_mass_out ? reinterpret_cast<float*>(w + p.row_lse) : nullptr;
   g.q_heads = n_q_heads;
   g.group = p.group;
-  g.rows_pad = p.rows_pad;
-  g.splits = p.splits;
-  g.split_len = p.split_len;
+  g.rows_max = p.rows_max;
+  g.pieces = p.pieces;
   g.scale2 = scale * 1.44269504088896341f;
   const bool half = dtype == SPLITZIP_KV4_FP16;
   if (cache->head_dim == 64) return half ? attend<64, true>(p, batch, g, stream) : attend<64, false>(p, batch, g, stream);

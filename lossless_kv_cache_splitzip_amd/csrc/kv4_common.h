@@ -86,16 +86,33 @@ struct Seq {
   bool ok;
 };
 
-__device__ inline Seq seq_of(const Batch& a, uint32_t b) {
+__device__ inline Seq seq_from(const Batch& a, int32_t len, int32_t row0, int32_t end) {
   Seq s;
-  s.len = a.lens[b];
-  s.row0 = a.cu ? a.cu[b] : (int32_t)b;
-  const int32_t end = a.cu ? a.cu[b + 1] : (int32_t)b + 1;
-  s.ok = s.len >= 0 && s.len <= (int32_t)a.max_len && s.row0 >= 0 && end >= s.row0 && end <= (int32_t)a.n_rows &&
-         (uint32_t)(end - s.row0) <= a.max_new;
-  s.rows = s.ok ? end - s.row0 : 0;
+  s.len = len;
+  s.row0 = row0;
+  s.ok = len >= 0 && len <= (int32_t)a.max_len && row0 >= 0 && end >= row0 && end <= (int32_t)a.n_rows &&
+         (uint32_t)(end - row0) <= a.max_new;
+  s.rows = s.ok ? end - row0 : 0;
   return s;
 }
+
+__device__ inline Seq seq_of(const Batch& a, uint32_t b) {
+  return seq_from(a, a.lens[b], a.cu ? a.cu[b] : (int32_t)b, a.cu ? a.cu[b + 1] : (int32_t)b + 1);
+}
+
+// Inclusive sums over the 64 lanes, in registers (row shifts, then the last
+// lane of 16 and of 32 to those behind).
+__device__ inline uint32_t wave_scan(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);  // row_shr:2
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);  // row_shr:4
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);  // row_shr:8
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);  // row_bcast:31
+  return v;
+}
+
+__device__ inline uint32_t wave_last(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
 
 // The page of table entry i of sequence b; a number outside the pool reads
 // page 0 and is reported.

@@ -115,21 +115,25 @@ def attention(q, pages, table, lens, cu, dim, scale, mass=None):
     return out, lse, mass, big, mag
 
 
-def attention_bounds(q, dim, lens, out, big, mag):
+def attention_bounds(q, dim, lens, out, big, mag, rows=0):
     """Largest error of out and of ln p that the kernels' arithmetic allows.
 
     A logit is a sum of D exact products in 32 bits (each addition off by at
     most 2^-24 of sum |q||k|), times scale log2 e (two roundings), then 2^x
     (a few units of 2^-23): |d ln p| <= (D + 4) 2^-24 sum|q||k| scale + 2^-21
     for the weight and the same for the sum that divides it.  The weights
-    enter the second product as two BF16 terms (16 bits, 2^-16), its sum over
+    enter the second product as two BF16 terms (16 bits, 2^-16), or, for BF16
+    queries with many `rows` (tokens x heads of a group) of a sequence, rounded
+    to BF16 once: each weight is then off by 2^-8 of itself at most and the
+    result by 2^-8 sum p|v|.  The sum over
     the slots is in 32 bits (L 2^-24), and the result is rounded once to the
     output's type.  A weight below 2^-126 relative to its row's largest is 0 in
     32 bits (2^-126 sum |v|), as is what BF16 leaves of it (as much again)."""
     longest = max([int(n) for n in lens] + [1])
     d = 2 * ((dim + 4) * 2.0 ** -24 * mag + 2.0 ** -21)
     final = torch.finfo(q.dtype).eps / 2
-    tol = final * out.abs() * (1 + 2.0 ** -8) + (d[..., None] + 2.0 ** -16 + longest * 2.0 ** -24) * big[0] * 1.01
+    weight = 2.0 ** -8 if q.dtype == torch.bfloat16 and rows > (16 if dim == 256 else 64) else 2.0 ** -16
+    tol = final * out.abs() * (1 + 2.0 ** -8) + (d[..., None] + weight + longest * 2.0 ** -24) * big[0] * 1.01
     tol = tol + 2.0 ** -125 * big[1]
     # below the type's normal range a rounding is half a subnormal step
     return tol + torch.finfo(q.dtype).smallest_normal * torch.finfo(q.dtype).eps, d

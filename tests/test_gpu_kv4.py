@@ -178,7 +178,7 @@ def _attend_case(lens, new, kv, group, dim, page, dtype, seed, scale=None, mass=
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     ro, rl, rm, big, mag = R.attention(q, pages.cpu(), table, ln, _cu(new), dim, scale, m_in)
-    tol, d = R.attention_bounds(q, dim, lens, ro, big, mag)
+    tol, d = R.attention_bounds(q, dim, lens, ro, big, mag, max(new + [0]) * group)
     err = (out[:rows].cpu().double() - ro).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
     if not strided:
