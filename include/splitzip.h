@@ -441,6 +441,7 @@ size_t splitzip_kv4_evict_work_bytes(const splitzip_kv4_cache* cache, const spli
  * those few tokens move; d_pos says which token a slot holds.
  *   batch       d_cu, max_new and n_rows are not read.
  *   sinks + recent <= budget, budget >= 1.
+ *   d_mass, d_pos, d_mass_out, d_pos_out  16-byte aligned.
  *   d_next_pos  [n_seqs] position that the sequence's next token will have.
  *   d_lens_out  [n_seqs] min(length, budget); may be d_lens.
  *   d_mass_out, d_pos_out  the slots below the new length; may be d_mass,

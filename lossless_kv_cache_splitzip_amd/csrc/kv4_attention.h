@@ -399,7 +399,7 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : kRows == 1 || D == 64 ?
   auto load_tile = [&](uint32_t it, Raw<D> (&r)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(2 * (it & 31) + h));
+      const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(2 * (it & 31) + h)) & ~kBadPage;
       const uint8_t* base = a.pages + ((uint64_t)p * a.n_heads + head) * a.page_bytes;
       load_raw<D, kRows == 1>(base, a.page_shift, __builtin_amdgcn_readfirstlane(slot_of(it, h)) & in_page, lane_at, r[h]);
     }
@@ -617,7 +617,7 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kern
   auto load_pages = [&](uint32_t t) { pages = page_of(a, b, slot_of(min(t + lane, n_tiles - 1)) >> a.page_shift); };
   Raw<D> raw;
   auto load_tile = [&](uint32_t t) {
-    const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(t & 63));
+    const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(t & 63)) & ~kBadPage;
     load_raw<D, false>(a.pages + ((uint64_t)p * a.n_heads + head) * a.page_bytes, a.page_shift,
                        __builtin_amdgcn_readfirstlane(slot_of(t)) & in_page, lane_at, raw);
   };
@@ -876,13 +876,16 @@ __global__ __launch_bounds__(kAttThreads, 2) void kv4_mass_kernel(AttArgs g) {
   auto load_tile = [&](uint32_t t, Raw<D> (&r)[4]) {
 #pragma unroll
     for (int h = 0; h < 4; ++h)
-      load_raw<D, true, false>(a.pages + ((uint64_t)page_at(t, h) * a.n_heads + head) * a.page_bytes, a.page_shift,
+      load_raw<D, true, false>(a.pages + ((uint64_t)(page_at(t, h) & ~kBadPage) * a.n_heads + head) * a.page_bytes, a.page_shift,
                                __builtin_amdgcn_readfirstlane(slot_of(t, h)) & in_page, lane_at, r[h]);
   };
-  // this lane's slot of a tile, as an index of the mass arrays
-  auto own_at = [&](uint32_t t) {
+  // this lane's slot of a tile, as an index of the mass arrays; none where there is nothing to write
+  constexpr uint64_t kNone = ~0ull;
+  auto own_at = [&](uint32_t t) -> uint64_t {
     const uint32_t p = j == 0 ? page_at(t, 0) : j == 1 ? page_at(t, 1) : j == 2 ? page_at(t, 2) : page_at(t, 3);
-    return (((uint64_t)p * a.n_heads + head) << a.page_shift) + ((first + 256 * t + lane) & in_page);
+    const uint32_t slot = first + 256 * t + lane;
+    if (slot >= c1 || (p & kBadPage)) return kNone;
+    return (((uint64_t)p * a.n_heads + head) << a.page_shift) + (slot & in_page);
   };
   auto compute = [&](uint32_t t, Raw<D> (&r)[4], uint64_t to, float old) {
     const uint32_t at = first + 256 * t;
@@ -912,12 +915,12 @@ __global__ __launch_bounds__(kAttThreads, 2) void kv4_mass_kernel(AttArgs g) {
       sum = sum_quarters(sum);
       own = (uint32_t)h == j ? sum : own;
     }
-    if (at + lane < c1) g.mass_out[to] = old + own;
+    if (to != kNone) g.mass_out[to] = old + own;
   };
   Raw<D> even[4], odd[4];
   auto step = [&](uint32_t t, Raw<D> (&cur)[4], Raw<D> (&nxt)[4]) {
     const uint64_t to = own_at(t);
-    const float old = first + 256 * t + lane < c1 ? g.mass[to] : 0.0f;
+    const float old = to != kNone ? g.mass[to] : 0.0f;
     const uint32_t ahead = min(t + 1, n_tiles - 1);
     if (((t + 1) & 15) == 0) load_pages(ahead);
     load_tile(ahead, nxt);
@@ -957,8 +960,8 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_mass_rows_k
     const uint32_t t = __builtin_amdgcn_readfirstlane(min(at + 16 * h, (len - 1) & ~15u));
     page[h] = page_of(a, b, t >> a.page_shift);
     Raw<D> raw;
-    load_raw<D, true, false>(a.pages + ((uint64_t)page[h] * a.n_heads + head) * a.page_bytes, a.page_shift, t & in_page,
-                             lane_at, raw);
+    load_raw<D, true, false>(a.pages + ((uint64_t)(page[h] & ~kBadPage) * a.n_heads + head) * a.page_bytes, a.page_shift,
+                             t & in_page, lane_at, raw);
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) k[h][st] = k_operand<D>(raw, st);
   }
@@ -1044,6 +1047,7 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_mass_rows_k
   }
   if (at + lane < len) {
     const uint32_t p = j == 0 ? page[0] : j == 1 ? page[1] : j == 2 ? page[2] : page[3];
+    if (p & kBadPage) return;
     const uint64_t to = (((uint64_t)p * a.n_heads + head) << a.page_shift) + ((at + lane) & in_page);
     g.mass_out[to] = g.mass[to] + own;
   }

@@ -1,7 +1,7 @@
 // The 4-bit cache's encoder and decoder (splitzip_kv4_append, splitzip_kv4_read).
 //
 // A lane holds 8 channels of one token of one head: one wide load, one code
-// dword.  Lanes run over the 4 tokens of a V group first, then over the
+// dword.  Lanes run over 4 tokens first, then over the
 // channels, so the stores of a wave fill whole runs of both code sections: V
 // codes interleave 4 tokens (kv4_common.h), K codes are a token's row.  A block
 // of 32 channels is then 4 lanes, 4 apart in a row of 16, whose largest
@@ -90,51 +90,88 @@ __device__ inline uint32_t encode8(float x[8], uint32_t& scale, bool& odd) {
 }
 
 // Where a lane of the row kernels works: its token, head and 8 channels.
-template <int D>
 struct Place {
   uint32_t b, slot, head, u;  // u: channels 8u .. 8u + 7
   uint64_t row;               // packed row
   uint8_t* base;              // the head's bytes in the slot's page
   uint32_t t;                 // slot in the page
   uint32_t page;
-  bool on;
+  bool on;  // false: nothing to do, or a page number outside the pool
 };
 
-template <int D>
-__device__ inline Place<D> place_of(const Batch& a) {
-  Place<D> p;
-  p.b = blockIdx.y;
-  p.on = false;
-  const Seq s = seq_of(a, p.b);
-  if (!s.ok || s.rows > s.len) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) corrupt(a.status);
-    return p;
+// The sequence of a packed row: the first whose rows end behind it.  64
+// sequences are looked at in one round of loads; the rows of a wave differ by
+// 3 at most, so one vote a row.
+__device__ inline uint32_t seq_of_row(const Batch& a, uint32_t row0, uint32_t t) {
+  if (!a.cu) return row0 + t;
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t seq = a.n_seqs;
+  for (uint32_t b = 0; b < a.n_seqs; b += 64) {
+    const int32_t end = b + lane < a.n_seqs ? a.cu[b + lane + 1] : 0;
+    uint32_t mine = a.n_seqs;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint64_t hit = __ballot(b + lane < a.n_seqs && end > (int32_t)(row0 + k));
+      if (k == t && hit) mine = b + (uint32_t)__builtin_ctzll(hit);
+    }
+    if (mine < seq) seq = mine;
+    if (__all(seq < a.n_seqs)) break;
   }
-  if (s.rows == 0) return p;
-  constexpr uint32_t kLanes = D / 2;  // of one group of 4 tokens of one head
-  const uint32_t first = (uint32_t)(s.len - s.rows);
-  const uint64_t w = (uint64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  const uint32_t gh = (uint32_t)(w / kLanes), lane = (uint32_t)(w % kLanes);
-  const uint32_t group = gh / a.n_heads;
+  return seq;
+}
+
+// Work item w: 4 packed rows, a head, 8 channels: D / 2 lanes for a head's 4
+// rows, rows fastest.  V codes keep 4 slots together, so rows that start at a
+// multiple of 4 fill whole words of 16 bytes, others two parts of them.  The
+// grid goes by the rows alone, whatever the batch's raggedness.
+template <int D>
+__device__ inline Place place_of(const Batch& a, uint64_t w) {
+  Place p;
+  constexpr uint32_t kLanes = D / 2;
+  const uint32_t gh = (uint32_t)(w / kLanes), lane = (uint32_t)(w % kLanes), t = lane & 3;
+  const uint32_t row0 = gh / a.n_heads * 4;
   p.head = gh % a.n_heads;
   p.u = lane >> 2;
-  p.slot = (first / 4 + group) * 4 + (lane & 3);
-  p.on = p.slot >= first && p.slot < (uint32_t)s.len;
+  p.row = row0 + t;
+  p.on = false;
+  // a wave's lanes may be of two heads (D = 64), of one group of rows unless the heads end: take the first lane's
+  const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)row0);
+  uint32_t b = seq_of_row(a, first, t);
+  if (__any(row0 != first)) {
+    const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)row0, 63);
+    const uint32_t b2 = seq_of_row(a, last, t);
+    if (row0 != first) b = b2;
+  }
+  if (p.row >= a.n_rows || b >= a.n_seqs) return p;
+  const Seq s = seq_of(a, b);
+  if (!s.ok || s.rows > s.len || p.row < (uint32_t)s.row0 || p.row >= (uint32_t)(s.row0 + s.rows)) return p;
+  p.b = b;
+  p.slot = (uint32_t)(s.len - s.rows) + (uint32_t)(p.row - s.row0);
+  p.page = page_of(a, b, p.slot >> a.page_shift);
+  p.on = p.page != kBadPage;
   if (!p.on) return p;
-  p.row = (uint64_t)s.row0 + (p.slot - first);
-  p.page = page_of(a, p.b, p.slot >> a.page_shift);
   p.t = p.slot & ((1u << a.page_shift) - 1);
   p.base = a.pages + ((uint64_t)p.page * a.n_heads + p.head) * a.page_bytes;
   return p;
+}
+
+// Reports sequences out of bounds: the last workgroup's job, as a bad one may
+// have no row that finds it.
+__device__ inline void report_bad(const Batch& a) {
+  if (blockIdx.x != gridDim.x - 1 || !a.status) return;
+  for (uint32_t b = threadIdx.x; b < a.n_seqs; b += kRowThreads) {
+    const Seq s = seq_of(a, b);
+    if (!s.ok || s.rows > s.len) corrupt(a.status);
+  }
 }
 
 template <int D, int T>
 __global__ __launch_bounds__(kRowThreads) void kv4_append_kernel(RowArgs r) {
   using L = Layout<D>;
   const Batch& a = r.a;
-  const Place<D> p = place_of<D>(a);
-  // a page number outside the pool: nothing is written
-  const bool on = p.on && (uint32_t)a.table[p.b * a.table_stride + (p.slot >> a.page_shift)] < a.n_pages;
+  report_bad(a);
+  const Place p = place_of<D>(a, (uint64_t)blockIdx.x * kRowThreads + threadIdx.x);
+  const bool on = p.on;
   float x[8] = {}, y[8] = {};
   if (on) {
     load8<T>(r.k, p.row * r.k_row + p.head * r.k_head + 8 * p.u, x);
@@ -200,7 +237,8 @@ template <int D, int T>
 __global__ __launch_bounds__(kRowThreads) void kv4_read_kernel(RowArgs r) {
   using L = Layout<D>;
   const Batch& a = r.a;
-  const Place<D> p = place_of<D>(a);
+  report_bad(a);
+  const Place p = place_of<D>(a, (uint64_t)blockIdx.x * kRowThreads + threadIdx.x);
   if (!p.on) return;
   const uint32_t sh = a.page_shift;
   const uint64_t at = (p.row * a.n_heads + p.head) * D + 8 * p.u;
@@ -225,10 +263,9 @@ __global__ __launch_bounds__(kRowThreads) void kv4_read_kernel(RowArgs r) {
   }
 }
 
-// Workgroups for the longest sequence's groups of 4 slots (one more than
-// max_new / 4 where both ends are partial); 0 for grids beyond 2^31.
+// Workgroups for all packed rows; 0 beyond 2^24.
 inline uint32_t row_blocks(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b) {
-  const uint64_t groups = ((uint64_t)b->max_new + 6) / 4;
+  const uint64_t groups = ((uint64_t)b->n_rows + 3) / 4;
   const uint64_t n = up(groups * c->n_heads * (c->head_dim / 2), kRowThreads) / kRowThreads;
   return n < (1ull << 24) ? (uint32_t)n : 0;
 }
@@ -297,7 +334,7 @@ int splitzip_kv4_append(const splitzip_kv4_cache* cache, const splitzip_kv4_batc
   r.positions = d_positions;
   r.mass = d_mass;
   r.pos = d_pos;
-  return dispatch<Append>(cache->head_dim, dtype, true, r, dim3(x, batch->n_seqs), stream);
+  return dispatch<Append>(cache->head_dim, dtype, true, r, dim3(x), stream);
 }
 
 int splitzip_kv4_read(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch, int dtype, void* d_k,
@@ -313,7 +350,7 @@ int splitzip_kv4_read(const splitzip_kv4_cache* cache, const splitzip_kv4_batch*
   r.a = batch_of(cache, batch, d_status);
   r.k_out = static_cast<uint8_t*>(d_k);
   r.v_out = static_cast<uint8_t*>(d_v);
-  return dispatch<Read>(cache->head_dim, dtype, false, r, dim3(x, batch->n_seqs), stream);
+  return dispatch<Read>(cache->head_dim, dtype, false, r, dim3(x), stream);
 }
 
 }  // extern "C"

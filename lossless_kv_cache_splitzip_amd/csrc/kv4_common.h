@@ -114,15 +114,16 @@ __device__ inline uint32_t wave_scan(uint32_t v) {
 
 __device__ inline uint32_t wave_last(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
 
-// The page of table entry i of sequence b; a number outside the pool reads
-// page 0 and is reported.
+// The page of table entry i of sequence b.  A number outside the pool is
+// reported and becomes page 0 with kBadPage set: to be read in its place
+// (results are unspecified then), never written.
+constexpr uint32_t kBadPage = 1u << 31;
+
 __device__ inline uint32_t page_of(const Batch& a, uint32_t b, uint32_t i) {
-  uint32_t p = (uint32_t)a.table[b * a.table_stride + i];
-  if (p >= a.n_pages) {
-    corrupt(a.status);
-    p = 0;
-  }
-  return p;
+  const uint32_t p = (uint32_t)a.table[b * a.table_stride + i];
+  if (p < a.n_pages) return p;
+  corrupt(a.status);
+  return kBadPage;
 }
 
 // Bytes inside one head's part of a page (P tokens, D channels).

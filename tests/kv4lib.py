@@ -151,8 +151,7 @@ def evict(pages, table, lens, mass, pos, next_pos, budget, sinks, recent, dim):
         pg, t = slots_of(table, b, n, page)
         for h in range(pages.shape[1]):
             keys = []
-            for i in range(n):
-                w, p = float(mass[pg[i], h, t[i]]), int(pos[pg[i], h, t[i]])
+            for i, (w, p) in enumerate(zip(old[1][pg, h, t].tolist(), old[2][pg, h, t].tolist())):
                 safe = p < sinks or p >= int(next_pos[b]) - recent
                 # protected slots rank equal, above all others
                 keys.append((0, 0.0, False, i) if safe else (1, math.inf if math.isnan(w) else -w, math.isnan(w), i))
@@ -161,11 +160,14 @@ def evict(pages, table, lens, mass, pos, next_pos, budget, sinks, recent, dim):
             holes = [i for i in range(budget) if i not in inside]
             movers = sorted(i for i in kept if i >= budget)
             assert len(holes) == len(movers)
-            for to, fr in zip(holes, movers):
-                for x, y in zip(places(dim, page, int(t[to])), places(dim, page, int(t[fr]))):
-                    pages[pg[to], h, x] = old[0][pg[fr], h, y]
-                mass[pg[to], h, t[to]] = old[1][pg[fr], h, t[fr]]
-                pos[pg[to], h, t[to]] = old[2][pg[fr], h, t[fr]]
+            if not holes:
+                continue
+            at = [places(dim, page, x) for x in range(page)]  # by slot in the page
+            at = torch.stack([torch.cat(x) for x in at])
+            to, fr = torch.tensor(holes), torch.tensor(movers)
+            pages[pg[to][:, None], h, at[t[to]]] = old[0][pg[fr][:, None], h, at[t[fr]]]
+            mass[pg[to], h, t[to]] = old[1][pg[fr], h, t[fr]]
+            pos[pg[to], h, t[to]] = old[2][pg[fr], h, t[fr]]
         lens[b] = budget
     return lens, pages, mass, pos
 

@@ -352,10 +352,36 @@ def _evict_case(lens, budget, sinks, recent, kv, dim, page, seed, in_place, spec
     ([300, 180], 7, 0, 0, 2, 256, 64),
     ([4097], 4096, 4, 64, 2, 128, 256),
     ([2500], 2000, 0, 2000, 1, 64, 16),
+    ([4096, 4095, 1100], 1024, 0, 4, 2, 64, 16),       # one round of slots, moves within the listed ones
+    ([8192, 5000], 2500, 4, 100, 1, 64, 32),           # two rounds, moves listed in memory
+    ([16384, 12289, 700], 16000, 4, 100, 1, 64, 128),  # four rounds
+    ([16385, 3], 300, 0, 10, 1, 64, 64),               # several workgroups a head
+    ([20000, 16400, 40000], 16390, 2, 50, 1, 64, 256),
 ])
 def test_evict_is_exact(lens, budget, sinks, recent, kv, dim, page, in_place):
     print(f"case evict {lens}->{budget} sinks={sinks} recent={recent} kv={kv} dim={dim} page={page}", flush=True)
     _evict_case(lens, budget, sinks, recent, kv, dim, page, 101, in_place)
+
+
+@pytest.mark.parametrize("n,budget", [(300, 100), (9000, 4500), (50000, 17), (50000, 30000)])
+@pytest.mark.parametrize("kind", ["equal", "two", "close", "one magnitude"])
+def test_evict_with_few_distinct_weights(n, budget, kind):
+    # ties over whole chunks, keys that differ in their last bits only
+    g = torch.Generator().manual_seed(n + budget)
+    n_pages = -(-n // 256)
+    table = torch.randperm(n_pages, generator=g).to(torch.int32)[None]
+    bits = {"equal": torch.zeros(n_pages, 1, 256, dtype=torch.int32),
+            "two": torch.randint(0, 2, (n_pages, 1, 256), generator=g, dtype=torch.int32) << 20,
+            "close": torch.randint(0, 50, (n_pages, 1, 256), generator=g, dtype=torch.int32),
+            "one magnitude": torch.randint(0, 1 << 23, (n_pages, 1, 256), generator=g, dtype=torch.int32)}[kind]
+    mass = (bits + 0x3F800000).view(torch.float32)
+    pos = torch.full((n_pages, 1, 256), 100, dtype=torch.int32)
+    pages = torch.randint(0, 256, (n_pages, 1, R.page_bytes(64, 256)), generator=g, dtype=torch.uint8)
+    ln, nxt = torch.tensor([n], dtype=torch.int32), torch.tensor([1000000], dtype=torch.int32)
+    want = R.evict(pages, table, ln, mass, pos, nxt, budget, 0, 5, 64)
+    d = [t.to(DEV) for t in (pages, table, ln, mass, pos, nxt)]
+    sz.kv4_evict(*d, 64, budget, recent=5)
+    assert torch.equal(d[2].cpu(), want[0]) and torch.equal(d[0].cpu(), want[1]) and torch.equal(d[3].cpu(), want[2])
 
 
 def test_evict_where_all_weights_are_equal_keeps_the_lowest_slots():
@@ -412,8 +438,13 @@ def test_bad_batches_are_reported_and_stay_in_bounds():
         pages.copy_(keep)
         if what != "cu":
             st.zero_()
-            sz.kv4_evict(pages, tb, ls.clone(), side.clone(), posn.clone(), ls, 64, 20, status=st)
+            m2, p2 = side.clone(), posn.clone()
+            sz.kv4_evict(pages, tb, ls.clone(), m2, p2, ls, 64, 20, status=st)
             assert int(st.item()) == sz.E_CORRUPT
+            # a page of no sequence is never written
+            used = torch.unique(table.long()).tolist()
+            for x in set(range(n)) - set(used):
+                assert torch.equal(m2[x], side[x]) and torch.equal(pages[x], keep[x])
             pages.copy_(keep)
     # more rows than slots: an error for append and read, empty rows for attention
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
