@@ -105,6 +105,28 @@ def test_append_matches_the_layout_and_read_gives_it_back(dim, page, kv, dtype, 
     assert torch.equal(hk.cpu(), kq.to(HF)) and torch.equal(hv.cpu(), vq.to(HF))
 
 
+@pytest.mark.parametrize("dtype", [HF, E5])
+def test_every_pattern_of_the_other_types(dtype):
+    """Each FP16 or E5M2 pattern as the first of a block of 2, -1.5, .. times it, and beside ones."""
+    bits = torch.arange(65536, dtype=torch.int32)
+    bits = bits.to(torch.int16).view(HF) if dtype == HF else bits[:256].to(torch.uint8).view(E5)
+    n = bits.numel()
+    x = torch.zeros(n, 2, 64)
+    x[:, 0] = bits.float()[:, None] * torch.linspace(-1, 1, 64)
+    x[:, 0, 0] = x[:, 0, 32] = bits.float()
+    x[:, 1, :32] = torch.linspace(0, 2, 32)
+    x[:, 1, 7] = bits.float()
+    x = x.to(dtype)
+    pages = _pool(n // 256, 2, 64, 256)
+    table = torch.arange(n // 256, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    sz.kv4_append(pages, x.to(DEV), x.to(DEV), table, lens, cu=cu)
+    k, v = sz.kv4_read(pages, table, lens, 64, cu=cu, n_tokens=n)
+    want = R.quantize(x.float())[0]
+    assert torch.equal(k.cpu().double(), want) and torch.equal(v.cpu().double(), want)
+
+
 def test_every_bf16_pattern_and_the_borders():
     # each of the 65,536 BF16 patterns as the largest of a block whose other
     # values sit at its rounding borders
@@ -149,6 +171,45 @@ def test_non_finite_values_are_stored_as_the_header_says():
         assert torch.equal(k.cpu().double(), R.quantize(y.float())[0])
     k = k.cpu().float()
     assert k[0, 0, 3] == 0 and k[1, 0, 40] == 1.5 and k[2, 0, 5] == -1.5 and k[3, 0, 0] == 1.0
+
+
+def test_many_sequences_some_without_rows():
+    """More sequences than a wave has lanes, rows of none, one and several."""
+    g = torch.Generator().manual_seed(9)
+    new = torch.randint(0, 4, (200,), generator=g).tolist()
+    new[0], new[63], new[64], new[199] = 0, 3, 0, 0
+    before = torch.randint(0, 40, (200,), generator=g).tolist()
+    lens = [a + b for a, b in zip(before, new)]
+    kv, dim, page = 3, 64, 16
+    n_pages = sum(-(-n // page) for n in lens)
+    table = R.table_of(lens, page, n_pages, 10)
+    pages = torch.zeros(n_pages, kv, R.page_bytes(dim, page), dtype=torch.uint8, device=DEV)
+    ln = torch.tensor(lens, dtype=torch.int32)
+    k, v = _rows(sum(lens), kv, dim, BF, 11, 0.3), _rows(sum(lens), kv, dim, BF, 12, 0.3)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    sz.kv4_append(pages, k.to(DEV), v.to(DEV), table.to(DEV), ln.to(DEV), cu=_cu(lens).to(DEV), status=st)
+    rk, rv = sz.kv4_read(pages, table.to(DEV), ln.to(DEV), dim, cu=_cu(new).to(DEV), n_tokens=sum(new), status=st)
+    assert int(st.item()) == 0
+    keep = torch.cat([torch.arange(e - m, e) for e, m in zip(np.cumsum(lens).tolist(), new)])
+    assert torch.equal(rk.cpu().double(), R.quantize(k.float())[0][keep])
+    assert torch.equal(rv.cpu().double(), R.quantize(v.float())[0][keep])
+    q = _rows(sum(new), 6, dim, BF, 13)
+    mass = torch.zeros(n_pages, kv, page, device=DEV)
+    out, lse = sz.kv4_attention(q.to(DEV), pages, table.to(DEV), ln.to(DEV), cu=_cu(new).to(DEV), max_new=3, mass=mass,
+                                return_lse=True, status=st)
+    assert int(st.item()) == 0
+    ro, rl, rm, big, mag = R.attention(q, pages.cpu(), table, ln, _cu(new), dim, dim ** -0.5, torch.zeros(n_pages, kv, page))
+    tol, d = R.attention_bounds(q, dim, lens, ro, big, mag)
+    assert bool(((out.cpu().double() - ro).abs() <= tol).all())
+    assert bool(((mass.cpu().double() - rm).abs() <= (float(d.max()) + 6 * 2.0 ** -24) * rm + 2.0 ** -23 * rm).all())
+    # long ones among short ones are cut, the short ones are not
+    budget = 20
+    nxt = torch.full((200,), 1000, dtype=torch.int32)
+    pos = torch.zeros(n_pages, kv, page, dtype=torch.int32)
+    want = R.evict(pages.cpu(), table, ln, mass.cpu(), pos, nxt, budget, 0, 0, dim)
+    d = [t.to(DEV) for t in (pages, table, ln, mass, pos, nxt)]
+    sz.kv4_evict(*d, dim, budget)
+    assert torch.equal(d[2].cpu(), want[0]) and torch.equal(d[0].cpu(), want[1])
 
 
 # ------------------------------------------------------------------- attention
