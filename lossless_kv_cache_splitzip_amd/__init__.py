@@ -50,7 +50,8 @@ def __getattr__(name):
     # the 4-bit cache's calls need torch from the start; the codec's import it when called
     if name in _KV4:
         from . import kv4
-        return getattr(kv4, name)
+        globals()[name] = value = getattr(kv4, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -37,6 +37,9 @@ constexpr uint32_t kMassPieces = 1536;
 // 64 rows of 128 channels, 16 x 8192 slots: 74 us against 82 through LDS; 128
 // rows: 165 against 132.
 constexpr uint32_t kFewRows = 64;
+// Up to this length a workgroup takes a head's slots whole: a second launch to
+// join pieces costs the host more than they save the GPU (1000 slots: equal).
+constexpr uint32_t kWholeLen = 1024;
 
 struct AttArgs {
   Batch a;
@@ -1073,9 +1076,10 @@ inline bool plan_of(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, ui
   const uint64_t round = (p->tile_rows >= 64 ? kManySlots : kFewSlots) / across;
   uint64_t pieces = round >= 4ull * b->n_seqs ? round - b->n_seqs : 2 * round;
   if (pieces < b->n_seqs) pieces = round ? b->n_seqs : 0;  // 0: enough rows to fill the GPU, no cut
+  if (p->tile_rows <= 32 && b->max_len <= kWholeLen) pieces = 0;
   // pieces are 128 slots or more
   const uint64_t most = (uint64_t)b->n_seqs * (up(b->max_len ? b->max_len : 1, 128) / 128);
-  p->grid = (uint32_t)(pieces + b->n_seqs < most ? pieces + b->n_seqs : most);
+  p->grid = pieces == 0 ? b->n_seqs : (uint32_t)(pieces + b->n_seqs < most ? pieces + b->n_seqs : most);
   p->pieces = (uint32_t)pieces;
   const uint64_t parts = p->grid > b->n_seqs ? (uint64_t)p->grid * c->n_heads * rows : 0;
   p->part_o = 0;

@@ -50,13 +50,13 @@ def _elsewhere(device, stream):
         if stream.device != device:
             raise ValueError(f"stream of {stream.device} for tensors on {device}")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():  # a device tensor exists, so the runtime is up
         return torch.cuda.device(device)
     return None
 
 
 def _tensor(t, name, dtype, shape, device):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr() or None
 
