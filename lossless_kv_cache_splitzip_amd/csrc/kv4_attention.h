@@ -52,6 +52,8 @@ struct AttArgs {
   float* part_o;    // [piece][head][rows_max][D] unnormalised sums
   float* part_ml;   // [piece][head][rows_max][2] largest logit (base 2), sum
   float* row_lse;   // [seq][head][rows_max] log2 of the sums, for the weights
+  float* mass_part; // [part][seq][head][max_len] weights of a part of the rows
+  uint32_t mass_parts;
   uint32_t q_heads, group;
   uint32_t rows_max;  // rows (token, head of the group) of the longest sequence
   uint32_t pieces;    // wanted in all (Piece); 0: sequences stay whole
@@ -572,10 +574,13 @@ constexpr int kWaveRows = D == 256 ? 16 : 32;
 // the grid, so that one head's row tiles meet in one XCD's L2 (8 heads), and
 // the last rows, which see the most, come first.
 template <int D, bool kHalf>
-__global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kernel(AttArgs g) {
+__global__ __launch_bounds__(kAttThreads, 2) void kv4_extend_kernel(AttArgs g) {
   constexpr int kSteps = D / 32, kChans = D / 16, kN = kWaveRows<D> / 16;
-  __shared__ u32x4 sh_k[2][4][kSteps][64];
-  __shared__ u32x2 sh_v[2][2][kChans][64][2];
+  // 16s of slots of a tile, its slots, its 32s.  256 channels: half a tile, so that two workgroups share a compute
+  // unit (6000 slots' prompts: 895 -> 631 us); two waves then have the keys and two the values to convert
+  constexpr int kKeys = D == 256 ? 2 : 4, kTile = 16 * kKeys, kPairs = kKeys / 2;
+  __shared__ u32x4 sh_k[2][kKeys][kSteps][64];
+  __shared__ u32x2 sh_v[2][kPairs][kChans][64][2];
   const Batch& a = g.a;
   const uint32_t head = blockIdx.x, tile = gridDim.y - 1 - blockIdx.y;
   const uint32_t tid = threadIdx.x, lane = tid & 63, i = lane & 15, j = lane >> 4;
@@ -613,9 +618,10 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kern
     for (int t = 0; t < kChans; ++t) o[n][t] = f32x4{0, 0, 0, 0};
   }
   // this wave's 16 slots of a tile; lane t holds the page of tile t, 64 tiles at a time
-  const uint32_t in_page = (1u << a.page_shift) - 1, n_tiles = c1 > c0 ? (c1 - c0 + 63) / 64 : 0;
+  const uint32_t in_page = (1u << a.page_shift) - 1, n_tiles = c1 > c0 ? (c1 - c0 + kTile - 1) / kTile : 0,
+                 mine = wave % kKeys;
   const LaneAt<D> lane_at(i, j);
-  auto slot_of = [&](uint32_t t) { return min(c0 + 64 * t + 16 * wave, (c1 - 1) & ~15u); };
+  auto slot_of = [&](uint32_t t) { return min(c0 + kTile * t + 16 * mine, (c1 - 1) & ~15u); };
   uint32_t pages = 0;
   auto load_pages = [&](uint32_t t) { pages = page_of(a, b, slot_of(min(t + lane, n_tiles - 1)) >> a.page_shift); };
   Raw<D> raw;
@@ -625,13 +631,17 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kern
                        __builtin_amdgcn_readfirstlane(slot_of(t)) & in_page, lane_at, raw);
   };
   auto convert = [&](uint32_t t) {  // raw -> LDS
-    const uint32_t at = c0 + 64 * t + 16 * wave, buf = t & 1;
+    const uint32_t at = c0 + kTile * t + 16 * mine, buf = t & 1;
     if (at + 16 > c1) clear_v<D>(raw, at + 4 * j, c1);
+    if (kKeys == 4 || wave < 2) {
 #pragma unroll
-    for (int st = 0; st < kSteps; ++st) sh_k[buf][wave][st][lane] = k_operand<D>(raw, st);
-    float sv[4];
-    v_scales4(raw.vs, sv);
-    v_to_lds<D, 0>(raw, sv, &sh_v[buf][wave >> 1][0][lane][wave & 1]);
+      for (int st = 0; st < kSteps; ++st) sh_k[buf][mine][st][lane] = k_operand<D>(raw, st);
+    }
+    if (kKeys == 4 || wave >= 2) {
+      float sv[4];
+      v_scales4(raw.vs, sv);
+      v_to_lds<D, 0>(raw, sv, &sh_v[buf][mine >> 1][0][lane][mine & 1]);
+    }
   };
   if (n_tiles > 0) {
     load_pages(0);
@@ -641,15 +651,18 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kern
   }
   for (uint32_t t = 0; t < n_tiles; ++t) {
     __syncthreads();
-    const uint32_t at = c0 + 64 * t, buf = t & 1;
+    const uint32_t at = c0 + kTile * t, buf = t & 1;
     if (at < w_last) {
-      f32x4 x[kN][4];
+      f32x4 x[kN][kKeys];
 #pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
+      for (int kt = 0; kt < kKeys; ++kt)
 #pragma unroll
         for (int n = 0; n < kN; ++n) x[n][kt] = f32x4{0, 0, 0, 0};
+      // steps outside: 8 sums in turn, so that none waits for its own last product
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
+      for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+        for (int kt = 0; kt < kKeys; ++kt) {
           const u32x4 k = sh_k[buf][kt][st][lane];
 #pragma unroll
           for (int n = 0; n < kN; ++n) {
@@ -657,22 +670,21 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kern
             if constexpr (kHalf) x[n][kt] = mma(k, ql[n][st], x[n][kt]);
           }
         }
-      }
-      if (at + 64 > w_first) {  // some row does not see all of the tile
+      if (at + kTile > w_first) {  // some row does not see all of the tile
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
-          for (int kt = 0; kt < 4; ++kt)
+          for (int kt = 0; kt < kKeys; ++kt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if ((int32_t)(at + 16 * kt + 4 * j + e) >= lim[n]) x[n][kt][e] = -INFINITY;
       }
-      u32x4 p[kN][2], pl[kN][2];
+      u32x4 p[kN][kPairs], pl[kN][kPairs];
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
         float top = m[n];
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int kt = 0; kt < kKeys; ++kt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = fmaxf(top, x[n][kt][e]);
         top = max_quarters(top);
@@ -685,7 +697,7 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kern
         }
         const float shift = m[n] == -INFINITY ? 0.0f : m[n] * g.scale2;
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int kt = 0; kt < kKeys; ++kt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float w0_ = __builtin_amdgcn_exp2f(fmaf(x[n][kt][2 * h], g.scale2, -shift));
@@ -698,7 +710,7 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_extend_kern
           }
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kPairs; ++h)
 #pragma unroll
         for (int c = 0; c < kChans; ++c) {
           const u32x4 v = *reinterpret_cast<const u32x4*>(&sh_v[buf][h][c][lane][0]);
@@ -938,21 +950,22 @@ __global__ __launch_bounds__(kAttThreads, 2) void kv4_mass_kernel(AttArgs g) {
 }
 
 // Many rows: 64 slots a wave stay in registers as operands, the query rows come
-// through LDS, 32 at a time for the four waves' 256 slots.
+// through LDS, 32 at a time for the four waves' 256 slots.  Where slots alone make too few workgroups the rows are shared too, and
+// kv4_mass_sum_kernel adds their parts.
 template <int D, bool kHalf>
 __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_mass_rows_kernel(AttArgs g) {
   constexpr int kSteps = D / 32, kTerms = kHalf ? 2 : 1, kMine = 2 * kSteps / 4;  // operands that a wave stages
   __shared__ u32x4 sh_q[2][kTerms][2 * kSteps][64];
   __shared__ float sh_lse[2][32];
   const Batch& a = g.a;
-  const uint32_t head = blockIdx.x, b = blockIdx.z;
+  const uint32_t head = blockIdx.x, b = blockIdx.z % a.n_seqs, part = blockIdx.z / a.n_seqs;
   const uint32_t tid = threadIdx.x, lane = tid & 63, i = lane & 15, j = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Seq s = seq_of(a, b);
   if (!s.ok) return;
   const uint32_t w_at = blockIdx.y * 256, at = w_at + 64 * wave, len = (uint32_t)s.len;
   if (w_at >= len) return;
-  const uint32_t rows = (uint32_t)s.rows * g.group;
+  const uint32_t all_rows = (uint32_t)s.rows * g.group;
   const int32_t before = s.len - s.rows;
   const uint32_t in_page = (1u << a.page_shift) - 1;
   const LaneAt<D> lane_at(i, j);
@@ -968,23 +981,26 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_mass_rows_k
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) k[h][st] = k_operand<D>(raw, st);
   }
-  // the first rows that see any of the workgroup's slots
+  // from the first rows that see any of the workgroup's slots, this part's rounds of 32
   const int32_t tok0 = (int32_t)w_at - before;
-  const uint32_t begin = tok0 > 0 ? (uint32_t)tok0 * g.group / 32 * 32 : 0;
+  const uint32_t from = tok0 > 0 ? (uint32_t)tok0 * g.group / 32 * 32 : 0;
+  const uint32_t share = (all_rows > from ? (all_rows - from + 32 * g.mass_parts - 1) / (32 * g.mass_parts) : 0) * 32;
+  const uint32_t begin = from + part * share, rows = min(all_rows, begin + share);
   u32x4 mh[kMine], ml[kMine];
   float m_lse = 0.0f;
-  auto fetch = [&](uint32_t r0) {  // rows r0 .. r0 + 31: global -> registers
+  auto fetch = [&](uint32_t r0) {  // rows r0 .. r0 + 31 (none beyond the last): global -> registers
 #pragma unroll
     for (int f = 0; f < kMine; ++f) {
       const uint32_t id = wave + 4 * f, r = r0 + 16 * (id / kSteps) + i;
       load_q_step<D, kHalf>(g, s, head, r, rows, j, id % kSteps, mh[f], ml[f]);
     }
     if (tid < 32) {
-      m_lse = r0 + tid < rows ? g.row_lse[(b * a.n_heads + head) * g.rows_max + r0 + tid] : INFINITY;
-      if (m_lse == -INFINITY) m_lse = INFINITY;  // a row without slots adds nothing
+      float v = r0 + tid < rows ? g.row_lse[(b * a.n_heads + head) * g.rows_max + r0 + tid] : INFINITY;
+      if (v == -INFINITY) v = INFINITY;  // a row without slots adds nothing
+      m_lse = v;
     }
   };
-  auto put = [&](uint32_t buf) {
+  auto put = [&](int buf) {
 #pragma unroll
     for (int f = 0; f < kMine; ++f) {
       sh_q[buf][0][wave + 4 * f][lane] = mh[f];
@@ -993,19 +1009,12 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_mass_rows_k
     if (tid < 32) sh_lse[buf][tid] = m_lse;
   };
   float sum[4] = {};
-  if (begin < rows) {
-    fetch(begin);
-    put(0);
-  }
-  uint32_t buf = 0;
-  for (uint32_t r0 = begin; r0 < rows; r0 += 32, buf ^= 1) {
-    __syncthreads();
-    if (r0 + 32 < rows) fetch(r0 + 32);
+  auto compute = [&](uint32_t r0, int buf) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const uint32_t ra = r0 + 16 * n;
       if (ra >= rows) continue;
-      const int32_t seen = before + (int32_t)(ra / g.group) + 1;                            // by the first row
+      const int32_t seen = before + (int32_t)(ra / g.group) + 1;                               // by the first row
       const int32_t most = before + (int32_t)(min(ra + 16, rows) - 1) / (int32_t)g.group + 1;  // and the last
       if (most <= (int32_t)at) continue;
       f32x4 x[4];
@@ -1040,7 +1049,20 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_mass_rows_k
         sum[h] += (w[0] + w[1]) + (w[2] + w[3]);
       }
     }
+  };
+  if (begin < rows) {
+    fetch(begin);
+    put(0);
+  }
+  auto round = [&](uint32_t r0, int buf) {
+    __syncthreads();
+    if (r0 + 32 < rows) fetch(r0 + 32);
+    compute(r0, buf);
     if (r0 + 32 < rows) put(buf ^ 1);
+  };
+  for (uint32_t r0 = begin; r0 < rows; r0 += 64) {
+    round(r0, 0);
+    if (r0 + 32 < rows) round(r0 + 32, 1);
   }
   float own = 0.0f;
 #pragma unroll
@@ -1048,18 +1070,37 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : 2) void kv4_mass_rows_k
     const float v = sum_quarters(sum[h]);
     own = (uint32_t)h == j ? v : own;
   }
-  if (at + lane < len) {
-    const uint32_t p = j == 0 ? page[0] : j == 1 ? page[1] : j == 2 ? page[2] : page[3];
-    if (p & kBadPage) return;
-    const uint64_t to = (((uint64_t)p * a.n_heads + head) << a.page_shift) + ((at + lane) & in_page);
-    g.mass_out[to] = g.mass[to] + own;
+  if (at + lane >= len) return;
+  if (g.mass_parts > 1) {
+    g.mass_part[(((uint64_t)part * a.n_seqs + b) * a.n_heads + head) * a.max_len + at + lane] = own;
+    return;
   }
+  const uint32_t p = j == 0 ? page[0] : j == 1 ? page[1] : j == 2 ? page[2] : page[3];
+  if (p & kBadPage) return;
+  const uint64_t to = (((uint64_t)p * a.n_heads + head) << a.page_shift) + ((at + lane) & in_page);
+  g.mass_out[to] = g.mass[to] + own;
+}
+
+__global__ __launch_bounds__(256) void kv4_mass_sum_kernel(AttArgs g) {
+  const Batch& a = g.a;
+  const uint32_t slot = blockIdx.x * 256 + threadIdx.x, head = blockIdx.y, b = blockIdx.z;
+  const Seq s = seq_of(a, b);
+  if (!s.ok || slot >= (uint32_t)s.len) return;
+  float sum = 0.0f;
+  for (uint32_t p = 0; p < g.mass_parts; ++p)
+    sum += g.mass_part[(((uint64_t)p * a.n_seqs + b) * a.n_heads + head) * a.max_len + slot];
+  const uint32_t page = page_of(a, b, slot >> a.page_shift);
+  if (page & kBadPage) return;
+  const uint64_t to = (((uint64_t)page * a.n_heads + head) << a.page_shift) + (slot & ((1u << a.page_shift) - 1));
+  g.mass_out[to] = g.mass[to] + sum;
 }
 
 // How a call is cut: rows per workgroup, pieces of the long axis.
 struct Plan {
   uint32_t group, rows_max, row_tiles, tile_rows, pieces, grid;
-  uint64_t part_o, part_ml, row_lse, bytes;  // offsets in the work area
+  bool mass_rows;       // the weights' kernel for many rows
+  uint32_t mass_parts;  // its shares of the rows
+  uint64_t part_o, part_ml, row_lse, mass_part, bytes;  // offsets in the work area
 };
 
 inline bool plan_of(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, uint32_t q_heads, bool mass, Plan* p) {
@@ -1085,7 +1126,17 @@ inline bool plan_of(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, ui
   p->part_o = 0;
   p->part_ml = up(parts * c->head_dim * 4, 256);
   p->row_lse = p->part_ml + up(parts * 8, 256);
-  p->bytes = p->row_lse + (mass ? up(n * 4, 256) : 0);
+  p->mass_part = p->row_lse + (mass ? up(n * 4, 256) : 0);
+  p->mass_rows = rows > (c->head_dim == 256 ? 16 : 64);
+  p->mass_parts = 1;
+  if (mass && p->mass_rows && n > 0) {
+    const uint64_t blocks = (uint64_t)b->n_seqs * c->n_heads * ((b->max_len + 255) / 256);
+    uint64_t parts_wanted = blocks >= kManySlots || blocks == 0 ? 1 : 2 * kManySlots / blocks;
+    if (parts_wanted > (rows + 127) / 128) parts_wanted = (rows + 127) / 128;
+    if (parts_wanted * b->n_seqs > 65535) parts_wanted = 1;
+    p->mass_parts = (uint32_t)parts_wanted;
+  }
+  p->bytes = p->mass_part + (p->mass_parts > 1 ? up((uint64_t)p->mass_parts * b->n_seqs * c->n_heads * b->max_len * 4, 256) : 0);
   if (p->bytes < 256) p->bytes = 256;
   return true;
 }
@@ -1112,7 +1163,7 @@ int attend(const Plan& p, const splitzip_kv4_batch* b, const AttArgs& g, hipStre
   }
   if (g.mass_out && b->max_len > 0) {
     const uint32_t rows = p.rows_max;
-    if (rows <= (D == 256 ? 16 : 64)) {
+    if (!p.mass_rows) {
       // pieces of their own: no results to join, so short ones, about 6 workgroups a compute unit
       AttArgs m = g;
       const uint64_t most = (uint64_t)b->n_seqs * ((b->max_len + 127) / 128);
@@ -1127,7 +1178,9 @@ int attend(const Plan& p, const splitzip_kv4_batch* b, const AttArgs& g, hipStre
       }
     } else {
       kv4_mass_rows_kernel<D, kHalf>
-          <<<dim3(g.a.n_heads, (b->max_len + 255) / 256, g.a.n_seqs), kAttThreads, 0, stream>>>(g);
+          <<<dim3(g.a.n_heads, (b->max_len + 255) / 256, g.a.n_seqs * p.mass_parts), kAttThreads, 0, stream>>>(g);
+      if (p.mass_parts > 1)
+        kv4_mass_sum_kernel<<<dim3((b->max_len + 255) / 256, g.a.n_heads, g.a.n_seqs), 256, 0, stream>>>(g);
     }
     if (hipGetLastError() != hipSuccess) return SPLITZIP_E_HIP;
   }
@@ -1176,6 +1229,8 @@ int splitzip_kv4_attention(const splitzip_kv4_cache* cache, const splitzip_kv4_b
   g.part_o = reinterpret_cast<float*>(w + p.part_o);
   g.part_ml = reinterpret_cast<float*>(w + p.part_ml);
   g.row_lse = d_mass_out ? reinterpret_cast<float*>(w + p.row_lse) : nullptr;
+  g.mass_part = reinterpret_cast<float*>(w + p.mass_part);
+  g.mass_parts = p.mass_parts;
   g.q_heads = n_q_heads;
   g.group = p.group;
   g.rows_max = p.rows_max;

@@ -280,6 +280,11 @@ SMALL = [
     ([97], [97], 2, 3, 256, 128, BF),
     ([260, 1], [129, 1], 1, 4, 256, 16, HF),
     ([700], [257], 2, 1, 64, 64, HF),
+    # many rows of few slots, shared between workgroups for the weights' sums
+    ([900], [900], 1, 4, 128, 32, BF),
+    ([600, 513], [600, 200], 1, 8, 64, 64, HF),
+    ([520], [300], 1, 2, 256, 16, HF),
+    ([1300, 200], [33, 40], 2, 2, 128, 64, BF),
 ]
 
 
