@@ -112,7 +112,8 @@ def load():
     lib.splitzip_pipeline_transfer.restype = i32
     lib.splitzip_compress_static.argtypes = [i32, vp, sz, vp, u32, sz, vp, sz, vp, vp]
     lib.splitzip_compress_static.restype = i32
-    cp, bp, f32 = ctypes.POINTER(KV4CacheDesc), ctypes.POINTER(KV4BatchDesc), ctypes.c_float
+    cp = bp = vp  # KV4CacheDesc, KV4BatchDesc by reference, or their bytes
+    f32 = ctypes.c_float
     lib.splitzip_kv4_page_bytes.argtypes = [u32, u32]
     lib.splitzip_kv4_page_bytes.restype = sz
     lib.splitzip_kv4_append.argtypes = [cp, bp, i32, vp, sz, sz, vp, sz, sz, vp, vp, vp, vp, vp]

@@ -18,16 +18,18 @@ for the work and for what is allocated.  Nothing is synchronized.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
 import torch
 
 from . import _native as N
 
-_byref = ctypes.byref
+# splitzip_kv4_cache and splitzip_kv4_batch as bytes: packing them costs a third of filling a ctypes structure
+_pack_cache = struct.Struct("@PIIII").pack
+_pack_batch = struct.Struct("@PNPPIIII").pack
 _HALF = {torch.bfloat16: N.BF16, torch.float16: N.KV4_FP16}
 _ROWS = {torch.bfloat16: N.BF16, torch.float16: N.KV4_FP16, torch.float8_e5m2: N.FP8_E5M2}
-_PAGES = (16, 32, 64, 128, 256)
+_PAGE_TOKENS = {(17 * d * p // 16, d): p for d in (64, 128, 256) for p in (16, 32, 64, 128, 256)}  # by bytes a head
 
 
 def kv4_page_bytes(head_dim: int, page_tokens: int) -> int:
@@ -58,7 +60,7 @@ def _elsewhere(device, stream):
 def _tensor(t, name, dtype, shape, device):
     if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t.data_ptr() or None
+    return t.data_ptr()
 
 
 def _optional(t, name, dtype, shape, device):
@@ -68,33 +70,36 @@ def _optional(t, name, dtype, shape, device):
 def _pool(pages):
     if not isinstance(pages, torch.Tensor) or not pages.is_cuda:
         raise ValueError("pages must be a device tensor")
-    if pages.dtype != torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
+    if pages.dtype is not torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
         raise ValueError("pages must be a contiguous uint8 tensor [n_pages, n_heads, page_bytes]")
     return pages.device
 
 
 def _cache(pages, head_dim):
+    """(splitzip_kv4_cache, shape of the side arrays)."""
     n, heads, size = pages.shape
-    p = size * 16 // (17 * head_dim) if head_dim > 0 else 0
-    if head_dim not in (64, 128, 256) or p not in _PAGES or size * 16 != 17 * head_dim * p:
+    p = _PAGE_TOKENS.get((size, head_dim))
+    if p is None:
         raise ValueError(f"pages of {size} bytes a head do not hold 16 to 256 tokens of head_dim {head_dim}")
-    return N.KV4CacheDesc(pages.data_ptr(), n, heads, head_dim, p)
+    return _pack_cache(pages.data_ptr(), n, heads, head_dim, p), (n, heads, p)
 
 
-def _batch(c, table, lens, cu, n_rows, max_new, max_len, device):
-    if table.dtype != torch.int32 or table.dim() != 2 or table.device != device or \
-            (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be an int32 tensor [n_seqs, pages] on {device} with contiguous rows")
+def _batch(page_tokens, table, lens, cu, n_rows, max_new, max_len, device):
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.device != device:
+        raise ValueError(f"table must be an int32 tensor [n_seqs, pages] on {device}")
     seqs, width = table.shape
-    stride = table.stride(0) if seqs > 1 else width
-    if stride < width:
-        raise ValueError("table's rows overlap")
+    stride, unit = table.stride()
+    if seqs <= 1:
+        stride = width
+    if (width > 1 and unit != 1) or stride < width:
+        raise ValueError("table's rows must be contiguous and must not overlap")
+    room = width * page_tokens
     if max_len is None:
-        max_len = width * c.page_tokens
-    elif not 0 <= max_len <= width * c.page_tokens:
-        raise ValueError(f"max_len {max_len} exceeds the table's {width} pages of {c.page_tokens} tokens")
+        max_len = min(room, 1 << 30)
+    elif not 0 <= max_len <= room:
+        raise ValueError(f"max_len {max_len} exceeds the table's {width} pages of {page_tokens} tokens")
     lens_at = _tensor(lens, "lens", torch.int32, (seqs,), device)
-    cu_at = None
+    cu_at = 0
     if cu is not None:
         cu_at = _tensor(cu, "cu", torch.int32, (seqs + 1,), device)
         max_new = n_rows if max_new is None else min(max_new, n_rows)
@@ -104,7 +109,7 @@ def _batch(c, table, lens, cu, n_rows, max_new, max_len, device):
         if n_rows != seqs:
             raise ValueError(f"{n_rows} rows for {seqs} sequences: several rows of a sequence need cu")
         max_new = min(1, n_rows)
-    return N.KV4BatchDesc(table.data_ptr() or None, stride, lens_at, cu_at, seqs, max_len, max_new, n_rows)
+    return _pack_batch(table.data_ptr(), stride, lens_at, cu_at, seqs, max_len, max_new, n_rows)
 
 
 def _strided(t, name, dtypes, heads, dim, device):
@@ -156,15 +161,14 @@ def kv4_append(pages, k, v, table, lens, cu=None, positions=None, mass=None, pos
         with ctx:
             return kv4_append(pages, k, v, table, lens, cu, positions, mass, pos, max_new, max_len, status)
     dim = k.shape[-1] if k.dim() == 3 else 0
-    c = _cache(pages, dim)
-    rows, k0, k1 = _strided(k, "k", _ROWS, c.n_heads, dim, device)
-    rows_v, v0, v1 = _strided(v, "v", (k.dtype,), c.n_heads, dim, device)
+    c, side = _cache(pages, dim)
+    rows, k0, k1 = _strided(k, "k", _ROWS, side[1], dim, device)
+    rows_v, v0, v1 = _strided(v, "v", (k.dtype,), side[1], dim, device)
     if rows_v != rows:
         raise ValueError(f"{rows} rows of k, {rows_v} of v")
-    side = (c.n_pages, c.n_heads, c.page_tokens)
-    b = _batch(c, table, lens, cu, rows, max_new, max_len, device)
+    b = _batch(side[2], table, lens, cu, rows, max_new, max_len, device)
     rc = N.load().splitzip_kv4_append(
-        _byref(c), _byref(b), _ROWS[k.dtype], k.data_ptr() or None, k0, k1, v.data_ptr() or None, v0, v1,
+        c, b, _ROWS[k.dtype], k.data_ptr(), k0, k1, v.data_ptr(), v0, v1,
         _optional(positions, "positions", torch.int32, (rows,), device),
         _optional(mass, "mass", torch.float32, side, device), _optional(pos, "pos", torch.int32, side, device),
         _status(status, device), _stream(device))
@@ -182,23 +186,23 @@ def kv4_read(pages, table, lens, head_dim, cu=None, n_tokens=None, dtype=torch.b
     if ctx is not None:
         with ctx:
             return kv4_read(pages, table, lens, head_dim, cu, n_tokens, dtype, max_new, max_len, out, status)
-    c = _cache(pages, head_dim)
+    c, side = _cache(pages, head_dim)
     if dtype not in _HALF:
         raise ValueError("dtype must be torch.bfloat16 or torch.float16")
     if n_tokens is None:
         if cu is not None:
             raise ValueError("n_tokens is needed with cu")
         n_tokens = table.shape[0]
-    shape = (n_tokens, c.n_heads, head_dim)
+    shape = (n_tokens, side[1], head_dim)
     if out is None:
         k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
     else:
         k, v = out
         _tensor(k, "out[0]", dtype, shape, device)
         _tensor(v, "out[1]", dtype, shape, device)
-    b = _batch(c, table, lens, cu, n_tokens, max_new, max_len, device)
-    rc = N.load().splitzip_kv4_read(_byref(c), _byref(b), _HALF[dtype], k.data_ptr() or None, v.data_ptr() or None,
-                                    _status(status, device), _stream(device))
+    b = _batch(side[2], table, lens, cu, n_tokens, max_new, max_len, device)
+    rc = N.load().splitzip_kv4_read(c, b, _HALF[dtype], k.data_ptr(), v.data_ptr(), _status(status, device),
+                                    _stream(device))
     _check(rc, "splitzip_kv4_read")
     return k, v
 
@@ -218,10 +222,10 @@ def kv4_attention(q, pages, table, lens, cu=None, max_new=None, scale=None, max_
             return kv4_attention(q, pages, table, lens, cu, max_new, scale, max_len, mass, mass_out, return_lse, out,
                                  lse, work, status)
     dim = q.shape[-1] if q.dim() == 3 else 0
-    c = _cache(pages, dim)
+    c, side = _cache(pages, dim)
     rows, q0, q1 = _strided(q, "q", _HALF, None, dim, device)
     heads = q.shape[1]
-    b = _batch(c, table, lens, cu, rows, max_new, max_len, device)
+    b = _batch(side[2], table, lens, cu, rows, max_new, max_len, device)
     if out is None:
         out = torch.empty((rows, heads, dim), dtype=q.dtype, device=device)
     else:
@@ -232,15 +236,13 @@ def kv4_attention(q, pages, table, lens, cu=None, max_new=None, scale=None, max_
         lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
     mass_at = to = None
     if mass is not None:
-        side = (c.n_pages, c.n_heads, c.page_tokens)
         mass_at = to = _tensor(mass, "mass", torch.float32, side, device)
         if mass_out is not None:
             to = _tensor(mass_out, "mass_out", torch.float32, side, device)
     elif mass_out is not None:
         raise ValueError("mass_out needs mass")
     lib = N.load()
-    cp, bp = _byref(c), _byref(b)
-    need = lib.splitzip_kv4_attention_work_bytes(cp, bp, heads, mass is not None)
+    need = lib.splitzip_kv4_attention_work_bytes(c, b, heads, mass is not None)
     if need == 0:
         raise N.SplitZipError(N.E_INVALID, "splitzip_kv4_attention_work_bytes")
     if work is None:
@@ -249,9 +251,9 @@ def kv4_attention(q, pages, table, lens, cu=None, max_new=None, scale=None, max_
         N._device_buffer(work, "work", need)
         if work.device != device:
             raise ValueError(f"work must be on {device}")
-    rc = lib.splitzip_kv4_attention(cp, bp, _HALF[q.dtype], q.data_ptr() or None, q0, q1, heads,
-                                    dim ** -0.5 if scale is None else scale, out.data_ptr() or None,
-                                    None if lse is None else lse.data_ptr() or None, mass_at, to, work.data_ptr(),
+    rc = lib.splitzip_kv4_attention(c, b, _HALF[q.dtype], q.data_ptr(), q0, q1, heads,
+                                    dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                                    None if lse is None else lse.data_ptr(), mass_at, to, work.data_ptr(),
                                     N._nbytes(work), _status(status, device), _stream(device))
     _check(rc, "splitzip_kv4_attention")
     return out if lse is None else (out, lse)
@@ -270,18 +272,16 @@ def kv4_evict(pages, table, lens, mass, pos, next_pos, head_dim, budget, sinks=0
         with ctx:
             return kv4_evict(pages, table, lens, mass, pos, next_pos, head_dim, budget, sinks, recent, max_len,
                              lens_out, mass_out, pos_out, work, status)
-    c = _cache(pages, head_dim)
+    c, side = _cache(pages, head_dim)
     seqs = table.shape[0]
-    side = (c.n_pages, c.n_heads, c.page_tokens)
     if min(budget, sinks, recent) < 0 or max(budget, sinks, recent) >= 1 << 32:
         raise ValueError("budget, sinks and recent must be 32-bit counts")
     lens_out = lens if lens_out is None else lens_out
     mass_out = mass if mass_out is None else mass_out
     pos_out = pos if pos_out is None else pos_out
-    b = _batch(c, table, lens, None, seqs, 1, max_len, device)
+    b = _batch(side[2], table, lens, None, seqs, 1, max_len, device)
     lib = N.load()
-    cp, bp = _byref(c), _byref(b)
-    need = lib.splitzip_kv4_evict_work_bytes(cp, bp, budget)
+    need = lib.splitzip_kv4_evict_work_bytes(c, b, budget)
     if need == 0:
         raise N.SplitZipError(N.E_INVALID, "splitzip_kv4_evict_work_bytes")
     if work is None:
@@ -291,7 +291,7 @@ def kv4_evict(pages, table, lens, mass, pos, next_pos, head_dim, budget, sinks=0
         if work.device != device:
             raise ValueError(f"work must be on {device}")
     rc = lib.splitzip_kv4_evict(
-        cp, bp, budget, sinks, recent, _tensor(next_pos, "next_pos", torch.int32, (seqs,), device),
+        c, b, budget, sinks, recent, _tensor(next_pos, "next_pos", torch.int32, (seqs,), device),
         _tensor(mass, "mass", torch.float32, side, device), _tensor(pos, "pos", torch.int32, side, device),
         _tensor(lens_out, "lens_out", torch.int32, (seqs,), device),
         _tensor(mass_out, "mass_out", torch.float32, side, device),
