@@ -29,9 +29,10 @@ constexpr int kAttThreads = 256;  // 4 waves
 // Workgroups that the GPU holds at once (256 compute units): the kernel for few
 // rows 3 a unit, by its registers; the one for many 2, by its LDS.
 constexpr uint32_t kFewSlots = 768, kManySlots = 512;
-// Pieces of the weights' sums: nothing to join, so short ones.  768, 1536, 3072
-// in all: 82.5, 81.8, 82.2 us (32 sequences), 60.6, 60.6, 71.8 (24, 35 rows).
-constexpr uint32_t kMassPieces = 1536;
+// Pieces of the weights' sums: nothing to join, so shorter ones, fewer where the
+// rows' operands take more registers.  480, 768, 1000, 1536 in all: 32.9, 29.8,
+// 28.8, 29.0 us (32 sequences of 4 rows), 12.5, 12.1, 14.4, 15.7 (24 of 35 rows).
+constexpr uint32_t kMassPieces = 1536, kMassPiecesRows = 768;
 // Up to so many rows every wave converts the cache for itself, in row tiles of
 // 32 (the second tile's reads are L2's): no barriers and more bytes under way.
 // 64 rows of 128 channels, 16 x 8192 slots: 74 us against 82 through LDS; 128
@@ -1164,16 +1165,17 @@ int attend(const Plan& p, const splitzip_kv4_batch* b, const AttArgs& g, hipStre
   if (g.mass_out && b->max_len > 0) {
     const uint32_t rows = p.rows_max;
     if (!p.mass_rows) {
-      // pieces of their own: no results to join, so short ones, about 6 workgroups a compute unit
+      // pieces of their own
       AttArgs m = g;
       const uint64_t most = (uint64_t)b->n_seqs * ((b->max_len + 127) / 128);
-      uint64_t pieces = kMassPieces / g.a.n_heads + 1;
+      uint64_t pieces = (rows <= 16 ? kMassPieces : kMassPiecesRows) / g.a.n_heads + 1;
       if (pieces < b->n_seqs) pieces = b->n_seqs;
       m.pieces = (uint32_t)pieces;
       const dim3 grid((uint32_t)(pieces + b->n_seqs < most ? pieces + b->n_seqs : most), g.a.n_heads);
       if (rows <= 16) kv4_mass_kernel<D, 1, kHalf><<<grid, kAttThreads, 0, stream>>>(m);
       if constexpr (D != 256) {
-        if (rows > 32) kv4_mass_kernel<D, 4, kHalf><<<grid, kAttThreads, 0, stream>>>(m);
+        if (rows > 48) kv4_mass_kernel<D, 4, kHalf><<<grid, kAttThreads, 0, stream>>>(m);
+        else if (rows > 32) kv4_mass_kernel<D, 3, kHalf><<<grid, kAttThreads, 0, stream>>>(m);
         else if (rows > 16) kv4_mass_kernel<D, 2, kHalf><<<grid, kAttThreads, 0, stream>>>(m);
       }
     } else {
