@@ -347,8 +347,8 @@ typedef struct {
   const int32_t* d_lens;  /* [n_seqs] slots in use */
   const int32_t* d_cu;    /* [n_seqs + 1] first packed row of each sequence; NULL: one row each (n_rows == n_seqs) */
   uint32_t n_seqs;        /* 0 .. 65535 */
-  uint32_t max_len;       /* no length is larger; up to 2^30 */
-  uint32_t max_new;       /* no sequence has more rows; <= n_rows */
+  uint32_t max_len;       /* no length is larger; up to 2^23 */
+  uint32_t max_new;       /* no sequence has more rows; 1 .. n_rows where there are rows */
   uint32_t n_rows;        /* rows of the packed tensors; up to 2^30 */
 } splitzip_kv4_batch;
 
@@ -418,8 +418,8 @@ size_t splitzip_kv4_attention_work_bytes(const splitzip_kv4_cache* cache, const 
  *              here leave one of their sums in them.
  *   d_work     splitzip_kv4_attention_work_bytes bytes, 256-byte aligned,
  *              overwritten; calls that may overlap need one each.
- * Weights and sums are held in 32 bits; for the product with V a weight counts
- * with 16 bits, or, in BF16 calls with more than 64 rows (tokens x query heads
+ * Logits have to be finite in 32 bits.  Weights and sums are held in 32 bits;
+ * for the product with V a weight counts with 16 bits, or, in BF16 calls with more than 64 rows (tokens x query heads
  * of a KV head; 16 where head_dim is 256), as BF16.  Only launches kernels, as the codec's
  * calls.  Returns SPLITZIP_OK, SPLITZIP_E_INVALID, SPLITZIP_E_CAPACITY (d_work
  * too small) or SPLITZIP_E_HIP. */

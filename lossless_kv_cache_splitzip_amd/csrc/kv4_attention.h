@@ -1119,6 +1119,7 @@ inline bool plan_of(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, ui
   uint64_t pieces = round >= 4ull * b->n_seqs ? round - b->n_seqs : 2 * round;
   if (pieces < b->n_seqs) pieces = round ? b->n_seqs : 0;  // 0: enough rows to fill the GPU, no cut
   if (p->tile_rows <= 32 && b->max_len <= kWholeLen) pieces = 0;
+  if (p->tile_rows >= 64 && pieces + b->n_seqs > 65535) pieces = 0;  // a grid's third dimension
   // pieces are 128 slots or more
   const uint64_t most = (uint64_t)b->n_seqs * (up(b->max_len ? b->max_len : 1, 128) / 128);
   p->grid = pieces == 0 ? b->n_seqs : (uint32_t)(pieces + b->n_seqs < most ? pieces + b->n_seqs : most);
@@ -1145,13 +1146,14 @@ inline bool plan_of(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, ui
 template <int D, bool kHalf>
 int attend(const Plan& p, const splitzip_kv4_batch* b, const AttArgs& g, hipStream_t stream) {
   const dim3 grid(p.grid, g.a.n_heads, p.row_tiles);
-  if (p.tile_rows >= 64) kv4_extend_kernel<D, kHalf><<<dim3(g.a.n_heads, p.row_tiles, p.grid), kAttThreads, 0, stream>>>(g);
+  // no row at all: only the weights' arrays are copied
+  if (p.rows_max > 0 && p.tile_rows >= 64) kv4_extend_kernel<D, kHalf><<<dim3(g.a.n_heads, p.row_tiles, p.grid), kAttThreads, 0, stream>>>(g);
   if constexpr (D != 256) {
-    if (p.tile_rows == 32) kv4_attend_kernel<D, 2, kHalf><<<grid, kAttThreads, 0, stream>>>(g);
+    if (p.rows_max > 0 && p.tile_rows == 32) kv4_attend_kernel<D, 2, kHalf><<<grid, kAttThreads, 0, stream>>>(g);
   }
-  if (p.tile_rows == 16) kv4_attend_kernel<D, 1, kHalf><<<grid, kAttThreads, 0, stream>>>(g);
+  if (p.rows_max > 0 && p.tile_rows == 16) kv4_attend_kernel<D, 1, kHalf><<<grid, kAttThreads, 0, stream>>>(g);
   if (hipGetLastError() != hipSuccess) return SPLITZIP_E_HIP;
-  if (p.grid > b->n_seqs) {
+  if (p.rows_max > 0 && p.grid > b->n_seqs) {
     // a workgroup a row until those fill the GPU
     if ((uint64_t)p.rows_max * g.a.n_heads * g.a.n_seqs <= 2048) {
       kv4_join_kernel<D, kHalf, true><<<dim3(p.rows_max, g.a.n_heads, g.a.n_seqs), 256, 0, stream>>>(g);

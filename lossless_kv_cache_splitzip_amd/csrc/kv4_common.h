@@ -20,7 +20,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr uint32_t kMaxSeqs = 65535, kMaxHeads = 1024, kMaxLen = 1u << 30, kMaxGroup = 64;
+// grids count sequences and 256s of slots in dimensions of up to 65535
+constexpr uint32_t kMaxSeqs = 65535, kMaxHeads = 1024, kMaxLen = 1u << 23, kMaxRows = 1u << 30, kMaxGroup = 64;
 
 inline uint64_t up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 
@@ -53,8 +54,8 @@ inline bool batch_ok(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, b
   if (!al(b->d_table, 4) || !al(b->d_lens, 4) || !al(b->d_cu, 4)) return false;
   if (b->n_seqs > 0 && (!b->d_lens || (b->max_len > 0 && !b->d_table))) return false;
   if (!rows) return true;
-  if (b->n_rows > kMaxLen || b->max_new > b->n_rows) return false;
-  return b->d_cu != nullptr || (b->n_rows == b->n_seqs && (b->n_rows == 0 || b->max_new >= 1));
+  if (b->n_rows > kMaxRows || b->max_new > b->n_rows || (b->n_rows > 0 && b->max_new == 0)) return false;
+  return b->d_cu != nullptr || b->n_rows == b->n_seqs;
 }
 
 inline Batch batch_of(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, int32_t* status) {

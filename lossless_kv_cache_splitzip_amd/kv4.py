@@ -95,7 +95,7 @@ def _batch(page_tokens, table, lens, cu, n_rows, max_new, max_len, device):
         raise ValueError("table's rows must be contiguous and must not overlap")
     room = width * page_tokens
     if max_len is None:
-        max_len = min(room, 1 << 30)
+        max_len = min(room, 1 << 23)
     elif not 0 <= max_len <= room:
         raise ValueError(f"max_len {max_len} exceeds the table's {width} pages of {page_tokens} tokens")
     lens_at = _tensor(lens, "lens", torch.int32, (seqs,), device)
@@ -103,8 +103,8 @@ def _batch(page_tokens, table, lens, cu, n_rows, max_new, max_len, device):
     if cu is not None:
         cu_at = _tensor(cu, "cu", torch.int32, (seqs + 1,), device)
         max_new = n_rows if max_new is None else min(max_new, n_rows)
-        if max_new < 0:
-            raise ValueError("max_new must not be negative")
+        if max_new < (n_rows > 0):
+            raise ValueError("max_new must be at least 1 where there are rows")
     else:
         if n_rows != seqs:
             raise ValueError(f"{n_rows} rows for {seqs} sequences: several rows of a sequence need cu")

@@ -328,6 +328,65 @@ def test_attention_shares_pages_and_repeats_bit_for_bit():
     assert bool(((outs[0][0].cpu().double() - ro).abs() <= tol).all())
 
 
+def test_attention_without_rows_copies_the_weights():
+    pages, table, ln = _filled([90, 5], 2, 64, 16, 85)
+    n = pages.shape[0]
+    mass, out = torch.rand(n, 2, 16, device=DEV), torch.full((n, 2, 16), -1.0, device=DEV)
+    cu = torch.zeros(3, dtype=torch.int32, device=DEV)
+    o = sz.kv4_attention(torch.zeros(0, 4, 64, dtype=BF, device=DEV), pages, table.to(DEV), ln.to(DEV), cu=cu, mass=mass,
+                         mass_out=out)
+    assert tuple(o.shape) == (0, 4, 64)
+    live = torch.zeros(n, 16, dtype=torch.bool)
+    for b, m in enumerate([90, 5]):
+        pg, t = R.slots_of(table, b, m, 16)
+        live[pg, t] = True
+    live = live[:, None].expand(-1, 2, -1).to(DEV)
+    assert torch.equal(out[live], mass[live]) and bool((out[~live] == -1).all())
+
+
+def test_arguments_that_do_not_fit_are_refused():
+    pages, table, ln = _filled([20, 30], 2, 64, 16, 86)
+    tb, ls = table.to(DEV), ln.to(DEV)
+    q, k = torch.zeros(2, 4, 64, dtype=BF, device=DEV), torch.zeros(2, 2, 64, dtype=BF, device=DEV)
+    n = pages.shape[0]
+    mass, pos = torch.zeros(n, 2, 16, device=DEV), torch.zeros(n, 2, 16, dtype=torch.int32, device=DEV)
+    bad = [
+        lambda: sz.kv4_attention(q.float(), pages, tb, ls),
+        lambda: sz.kv4_attention(q[:, :3], pages, tb, ls),                       # heads of no group
+        lambda: sz.kv4_attention(q[:1], pages, tb, ls),                          # one row for two sequences
+        lambda: sz.kv4_attention(q[..., :32], pages, tb, ls),
+        lambda: sz.kv4_attention(q, pages[:, :, :-16], tb, ls),
+        lambda: sz.kv4_attention(q, pages, tb.long(), ls),
+        lambda: sz.kv4_attention(q, pages, tb, ls[:1]),
+        lambda: sz.kv4_attention(q, pages, tb, ls, max_len=10 ** 6),
+        lambda: sz.kv4_attention(q, pages, tb, ls, mass=mass[:1]),
+        lambda: sz.kv4_attention(q, pages, tb, ls, mass_out=mass),
+        lambda: sz.kv4_attention(q, pages, tb, ls, out=q[:, :2]),
+        lambda: sz.kv4_attention(q, pages, tb, ls, scale=0.0),
+        lambda: sz.kv4_attention(q, pages, tb, ls, work=torch.zeros(8, dtype=torch.uint8, device=DEV)),
+        lambda: sz.kv4_attention(q.transpose(0, 2), pages, tb, ls),
+        lambda: sz.kv4_attention(torch.zeros(2, 4, 65, dtype=BF, device=DEV)[..., 1:], pages, tb, ls),
+        lambda: sz.kv4_attention(q, pages, tb, ls, cu=torch.zeros(3, dtype=torch.int32, device=DEV), max_new=0),
+        lambda: sz.kv4_append(pages, k, k[:1], tb, ls),
+        lambda: sz.kv4_append(pages, k, k.half(), tb, ls),
+        lambda: sz.kv4_append(pages, k[:, :1], k[:, :1], tb, ls),
+        lambda: sz.kv4_append(pages, k, k, tb, ls, positions=torch.zeros(3, dtype=torch.int32, device=DEV)),
+        lambda: sz.kv4_append(pages, k, k, tb, ls, status=torch.zeros(1, device=DEV)),
+        lambda: sz.kv4_read(pages, tb, ls, 128),
+        lambda: sz.kv4_read(pages, tb, ls, 64, dtype=torch.float32),
+        lambda: sz.kv4_read(pages, tb, ls, 64, cu=torch.zeros(3, dtype=torch.int32, device=DEV)),
+        lambda: sz.kv4_evict(pages, tb, ls, mass, pos, ls, 64, 0),
+        lambda: sz.kv4_evict(pages, tb, ls, mass, pos, ls, 64, 8, sinks=5, recent=4),
+        lambda: sz.kv4_evict(pages, tb, ls, mass, pos, ls, 64, -1),
+        lambda: sz.kv4_evict(pages, tb, ls, mass[: n - 1], pos, ls, 64, 8),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, sz.SplitZipError)):
+            call()
+            print("accepted", i, flush=True)
+    torch.cuda.synchronize()
+
+
 def test_attention_mass_accumulates_in_place():
     pages, table, ln = _filled([90, 200], 2, 64, 16, 81)
     q = _rows(2, 4, 64, BF, 82).to(DEV)

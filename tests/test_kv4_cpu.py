@@ -26,9 +26,9 @@ BAD_CACHES = [dict(d_pages=None), dict(d_pages=P + 8), dict(n_pages=0), dict(n_p
               dict(n_heads=1025), dict(head_dim=0), dict(head_dim=96), dict(head_dim=512), dict(page_tokens=8),
               dict(page_tokens=24), dict(page_tokens=512)]
 BAD_BATCHES = [dict(d_table=None), dict(d_lens=None), dict(d_lens=P + 2), dict(d_table=P + 1), dict(table_stride=3),
-               dict(n_seqs=65536), dict(max_len=(1 << 30) + 1, table_stride=1 << 30)]
+               dict(n_seqs=65536), dict(max_len=(1 << 23) + 1, table_stride=1 << 30)]
 BAD_ROWS = [dict(d_cu=P + 2), dict(max_new=8), dict(n_rows=(1 << 30) + 1), dict(d_cu=None),
-            dict(d_cu=None, n_rows=3, max_new=0)]
+            dict(d_cu=None, n_rows=3, max_new=0), dict(max_new=0)]
 
 
 def append(c, b, **kw):
@@ -94,6 +94,12 @@ def test_attention_refusals():
     assert need > 256 and need % 256 == 0
     assert attention(cache(), b, mass=P, mass_out=P, bytes=need - 1) == sz.E_CAPACITY
     assert attention(cache(), batch(n_seqs=0)) == sz.OK
+    # the largest batches have a plan, with a workspace that fits the card
+    for kw in (dict(n_seqs=65535, n_rows=65535, max_new=1, d_cu=None, max_len=1 << 23, table_stride=1 << 19),
+               dict(n_seqs=60000, n_rows=1 << 20, max_new=40, max_len=4096, table_stride=256),
+               dict(n_seqs=1, n_rows=1 << 17, max_new=1 << 17, max_len=1 << 17, table_stride=1 << 13)):
+        need = N.load().splitzip_kv4_attention_work_bytes(ctypes.byref(cache()), ctypes.byref(batch(**kw)), 8, 1)
+        assert 0 < need < 64 << 30, (kw, need)
     assert attention(cache(), batch(max_new=0, n_rows=0)) == sz.OK
 
 
