@@ -7,7 +7,7 @@
 // lanes, 4 apart in a row of 16, whose largest magnitude two row rotations give.
 // Both kernels move each byte once and are bound by memory, for a few rows by
 // the launch and the chain lengths -> block table -> page (64 rows: 4.0 and 3.5
-// us).  21,251 rows of 8 heads of 128 BF16 channels: append 25 us for 111 MB,
+// us).  21,249 rows of 8 heads of 128 BF16 channels: append 25 us for 111 MB,
 // read 20.5 us for 110 MB.
 #ifndef SPLITZIP_KV4_CODEC_H
 #define SPLITZIP_KV4_CODEC_H
@@ -283,7 +283,7 @@ __device__ inline u32x4 decode8(uint32_t c, uint32_t scale) {
   return o;
 }
 
-// The rows are not read again here: past the caches (34,000 rows: 45.8 -> 29.4 us between other work).
+// The rows are not read again here: past the caches (24,348 rows: 45.8 -> 29.4 us between other work).
 __device__ inline void put16(uint8_t* p, u32x4 v) { __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p)); }
 
 template <int D, int T>
