@@ -45,49 +45,53 @@ def kv4_pages(n_pages: int, n_heads: int, head_dim: int, page_tokens: int, devic
     return torch.zeros(n_pages, n_heads, kv4_page_bytes(head_dim, page_tokens), dtype=torch.uint8, device=device)
 
 
-def _elsewhere(device, stream):
+# `dev` below is a device's index: comparing get_device() costs half of comparing devices
+
+def _elsewhere(dev, stream):
     """The context to run in when the call is not for the current device and
     stream, else None."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        if stream.device.index != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
         return torch.cuda.stream(stream)
-    if device.index != torch._C._cuda_getDevice():  # a device tensor exists, so the runtime is up
-        return torch.cuda.device(device)
+    if dev != torch._C._cuda_getDevice():  # a device tensor exists, so the runtime is up
+        return torch.cuda.device(dev)
     return None
 
 
-def _tensor(t, name, dtype, shape, device):
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+def _tensor(t, name, dtype, shape, dev):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _optional(t, name, dtype, shape, device):
-    return None if t is None else _tensor(t, name, dtype, shape, device)
+def _optional(t, name, dtype, shape, dev):
+    return None if t is None else _tensor(t, name, dtype, shape, dev)
 
 
 def _pool(pages):
     if not isinstance(pages, torch.Tensor) or not pages.is_cuda:
         raise ValueError("pages must be a device tensor")
-    if pages.dtype is not torch.uint8 or pages.dim() != 3 or not pages.is_contiguous():
-        raise ValueError("pages must be a contiguous uint8 tensor [n_pages, n_heads, page_bytes]")
-    return pages.device
+    return pages.get_device()
 
 
 def _cache(pages, head_dim):
     """(splitzip_kv4_cache, shape of the side arrays)."""
-    n, heads, size = pages.shape
+    shape = pages.shape
+    if len(shape) != 3 or pages.dtype is not torch.uint8 or not pages.is_contiguous():
+        raise ValueError("pages must be a contiguous uint8 tensor [n_pages, n_heads, page_bytes]")
+    n, heads, size = shape
     p = _PAGE_TOKENS.get((size, head_dim))
     if p is None:
         raise ValueError(f"pages of {size} bytes a head do not hold 16 to 256 tokens of head_dim {head_dim}")
     return _pack_cache(pages.data_ptr(), n, heads, head_dim, p), (n, heads, p)
 
 
-def _batch(page_tokens, table, lens, cu, n_rows, max_new, max_len, device):
-    if table.dtype is not torch.int32 or table.dim() != 2 or table.device != device:
-        raise ValueError(f"table must be an int32 tensor [n_seqs, pages] on {device}")
-    seqs, width = table.shape
+def _batch(page_tokens, table, lens, cu, n_rows, max_new, max_len, dev):
+    shape = table.shape
+    if len(shape) != 2 or table.dtype is not torch.int32 or table.get_device() != dev:
+        raise ValueError(f"table must be an int32 tensor [n_seqs, pages] on cuda:{dev}")
+    seqs, width = shape
     stride, unit = table.stride()
     if seqs <= 1:
         stride = width
@@ -98,10 +102,10 @@ def _batch(page_tokens, table, lens, cu, n_rows, max_new, max_len, device):
         max_len = min(room, 1 << 23)
     elif not 0 <= max_len <= room:
         raise ValueError(f"max_len {max_len} exceeds the table's {width} pages of {page_tokens} tokens")
-    lens_at = _tensor(lens, "lens", torch.int32, (seqs,), device)
+    lens_at = _tensor(lens, "lens", torch.int32, (seqs,), dev)
     cu_at = 0
     if cu is not None:
-        cu_at = _tensor(cu, "cu", torch.int32, (seqs + 1,), device)
+        cu_at = _tensor(cu, "cu", torch.int32, (seqs + 1,), dev)
         max_new = n_rows if max_new is None else min(max_new, n_rows)
         if max_new < (n_rows > 0):
             raise ValueError("max_new must be at least 1 where there are rows")
@@ -112,13 +116,14 @@ def _batch(page_tokens, table, lens, cu, n_rows, max_new, max_len, device):
     return _pack_batch(table.data_ptr(), stride, lens_at, cu_at, seqs, max_len, max_new, n_rows)
 
 
-def _strided(t, name, dtypes, heads, dim, device):
-    """(rows, row stride, head stride) of t [rows, heads, dim]."""
-    if t.dtype not in dtypes or t.dim() != 3 or t.device != device:
-        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor of {' or '.join(map(str, dtypes))} on {device}")
-    rows, h, d = t.shape
+def _strided(t, name, dtypes, heads, dim, dev):
+    """(rows, row stride, head stride, address) of t [rows, heads, dim]."""
+    shape = t.shape
+    if len(shape) != 3 or t.dtype not in dtypes or t.get_device() != dev:
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor of {' or '.join(map(str, dtypes))} on cuda:{dev}")
+    rows, h, d = shape
     if d != dim or (heads is not None and h != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, heads {heads} and head_dim {dim} expected")
+        raise ValueError(f"{name} has shape {tuple(shape)}, heads {heads} and head_dim {dim} expected")
     s0, s1, s2 = t.stride()
     if s2 != 1:
         raise ValueError(f"{name}'s channels must be contiguous")
@@ -126,9 +131,10 @@ def _strided(t, name, dtypes, heads, dim, device):
         s0 = 0
     if h <= 1:
         s1 = 0
-    if (s0 | s1) & 7 or t.data_ptr() % (8 * t.element_size()):
+    at = t.data_ptr()
+    if (s0 | s1) & 7 or at % (8 * t.element_size()):
         raise ValueError(f"{name}'s rows and heads must start at multiples of 8 elements")
-    return rows, s0, s1
+    return rows, s0, s1, at
 
 
 def _check(rc, what):
@@ -136,17 +142,25 @@ def _check(rc, what):
         raise N.SplitZipError(rc, what)
 
 
-def _stream(device):
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _status(status, device):
+def _status(status, dev):
     if status is None:
         return None
     N._status_word(status)
-    if status.device != device:
-        raise ValueError(f"status must be on {device}")
+    if status.get_device() != dev:
+        raise ValueError(f"status must be on cuda:{dev}")
     return status.data_ptr()
+
+
+def _work(work, need, dev):
+    if work is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    N._device_buffer(work, "work", need)
+    if work.get_device() != dev:
+        raise ValueError(f"work must be on cuda:{dev}")
+    return work
 
 
 def kv4_append(pages, k, v, table, lens, cu=None, positions=None, mass=None, pos=None, max_new=None, max_len=None,
@@ -155,23 +169,23 @@ def kv4_append(pages, k, v, table, lens, cu=None, positions=None, mass=None, pos
     float8_e5m2, strided views allowed) into their sequences' last slots.
     ``mass`` of the slots becomes 0 and ``pos`` the rows' ``positions`` (int32
     [rows]; None: the slot's number)."""
-    device = _pool(pages)
-    ctx = _elsewhere(device, stream)
+    dev = _pool(pages)
+    ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return kv4_append(pages, k, v, table, lens, cu, positions, mass, pos, max_new, max_len, status)
     dim = k.shape[-1] if k.dim() == 3 else 0
     c, side = _cache(pages, dim)
-    rows, k0, k1 = _strided(k, "k", _ROWS, side[1], dim, device)
-    rows_v, v0, v1 = _strided(v, "v", (k.dtype,), side[1], dim, device)
+    rows, k0, k1, k_at = _strided(k, "k", _ROWS, side[1], dim, dev)
+    rows_v, v0, v1, v_at = _strided(v, "v", (k.dtype,), side[1], dim, dev)
     if rows_v != rows:
         raise ValueError(f"{rows} rows of k, {rows_v} of v")
-    b = _batch(side[2], table, lens, cu, rows, max_new, max_len, device)
+    b = _batch(side[2], table, lens, cu, rows, max_new, max_len, dev)
     rc = N.load().splitzip_kv4_append(
-        c, b, _ROWS[k.dtype], k.data_ptr(), k0, k1, v.data_ptr(), v0, v1,
-        _optional(positions, "positions", torch.int32, (rows,), device),
-        _optional(mass, "mass", torch.float32, side, device), _optional(pos, "pos", torch.int32, side, device),
-        _status(status, device), _stream(device))
+        c, b, _ROWS[k.dtype], k_at, k0, k1, v_at, v0, v1,
+        _optional(positions, "positions", torch.int32, (rows,), dev),
+        _optional(mass, "mass", torch.float32, side, dev), _optional(pos, "pos", torch.int32, side, dev),
+        _status(status, dev), _stream(dev))
     _check(rc, "splitzip_kv4_append")
 
 
@@ -181,8 +195,8 @@ def kv4_read(pages, table, lens, head_dim, cu=None, n_tokens=None, dtype=torch.b
     inverse of ``kv4_append``.  ``n_tokens``: packed rows in all (cu[-1]; the
     number of sequences where cu is None).  ``out``: the two tensors to fill;
     rows of no sequence are not written."""
-    device = _pool(pages)
-    ctx = _elsewhere(device, stream)
+    dev = _pool(pages)
+    ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return kv4_read(pages, table, lens, head_dim, cu, n_tokens, dtype, max_new, max_len, out, status)
@@ -195,14 +209,14 @@ def kv4_read(pages, table, lens, head_dim, cu=None, n_tokens=None, dtype=torch.b
         n_tokens = table.shape[0]
     shape = (n_tokens, side[1], head_dim)
     if out is None:
-        k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
+        k, v = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
     else:
         k, v = out
-        _tensor(k, "out[0]", dtype, shape, device)
-        _tensor(v, "out[1]", dtype, shape, device)
-    b = _batch(side[2], table, lens, cu, n_tokens, max_new, max_len, device)
-    rc = N.load().splitzip_kv4_read(c, b, _HALF[dtype], k.data_ptr(), v.data_ptr(), _status(status, device),
-                                    _stream(device))
+        _tensor(k, "out[0]", dtype, shape, dev)
+        _tensor(v, "out[1]", dtype, shape, dev)
+    b = _batch(side[2], table, lens, cu, n_tokens, max_new, max_len, dev)
+    rc = N.load().splitzip_kv4_read(c, b, _HALF[dtype], k.data_ptr(), v.data_ptr(), _status(status, dev),
+                                    _stream(dev))
     _check(rc, "splitzip_kv4_read")
     return k, v
 
@@ -215,46 +229,41 @@ def kv4_attention(q, pages, table, lens, cu=None, max_new=None, scale=None, max_
     ``lse`` given.  ``scale`` defaults to head_dim ** -0.5.  With ``mass``, the
     weights that every slot drew are added into ``mass_out`` (default: into
     ``mass``).  Rows of no sequence are not written."""
-    device = _pool(pages)
-    ctx = _elsewhere(device, stream)
+    dev = _pool(pages)
+    ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return kv4_attention(q, pages, table, lens, cu, max_new, scale, max_len, mass, mass_out, return_lse, out,
                                  lse, work, status)
     dim = q.shape[-1] if q.dim() == 3 else 0
     c, side = _cache(pages, dim)
-    rows, q0, q1 = _strided(q, "q", _HALF, None, dim, device)
+    rows, q0, q1, q_at = _strided(q, "q", _HALF, None, dim, dev)
     heads = q.shape[1]
-    b = _batch(side[2], table, lens, cu, rows, max_new, max_len, device)
+    b = _batch(side[2], table, lens, cu, rows, max_new, max_len, dev)
     if out is None:
-        out = torch.empty((rows, heads, dim), dtype=q.dtype, device=device)
+        out = torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
     else:
-        _tensor(out, "out", q.dtype, (rows, heads, dim), device)
+        _tensor(out, "out", q.dtype, (rows, heads, dim), dev)
     if lse is not None:
-        _tensor(lse, "lse", torch.float32, (rows, heads), device)
+        _tensor(lse, "lse", torch.float32, (rows, heads), dev)
     elif return_lse:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
     mass_at = to = None
     if mass is not None:
-        mass_at = to = _tensor(mass, "mass", torch.float32, side, device)
+        mass_at = to = _tensor(mass, "mass", torch.float32, side, dev)
         if mass_out is not None:
-            to = _tensor(mass_out, "mass_out", torch.float32, side, device)
+            to = _tensor(mass_out, "mass_out", torch.float32, side, dev)
     elif mass_out is not None:
         raise ValueError("mass_out needs mass")
     lib = N.load()
     need = lib.splitzip_kv4_attention_work_bytes(c, b, heads, mass is not None)
     if need == 0:
         raise N.SplitZipError(N.E_INVALID, "splitzip_kv4_attention_work_bytes")
-    if work is None:
-        work = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        N._device_buffer(work, "work", need)
-        if work.device != device:
-            raise ValueError(f"work must be on {device}")
-    rc = lib.splitzip_kv4_attention(c, b, _HALF[q.dtype], q.data_ptr(), q0, q1, heads,
+    work = _work(work, need, dev)
+    rc = lib.splitzip_kv4_attention(c, b, _HALF[q.dtype], q_at, q0, q1, heads,
                                     dim ** -0.5 if scale is None else scale, out.data_ptr(),
                                     None if lse is None else lse.data_ptr(), mass_at, to, work.data_ptr(),
-                                    N._nbytes(work), _status(status, device), _stream(device))
+                                    N._nbytes(work), _status(status, dev), _stream(dev))
     _check(rc, "splitzip_kv4_attention")
     return out if lse is None else (out, lse)
 
@@ -266,8 +275,8 @@ def kv4_evict(pages, table, lens, mass, pos, next_pos, head_dim, budget, sinks=0
     ``sinks`` or at ``next_pos`` - ``recent`` and beyond always stay.  Returns
     ``(lens_out, mass_out, pos_out)``, by default the tensors given, updated in
     place."""
-    device = _pool(pages)
-    ctx = _elsewhere(device, stream)
+    dev = _pool(pages)
+    ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return kv4_evict(pages, table, lens, mass, pos, next_pos, head_dim, budget, sinks, recent, max_len,
@@ -279,23 +288,18 @@ def kv4_evict(pages, table, lens, mass, pos, next_pos, head_dim, budget, sinks=0
     lens_out = lens if lens_out is None else lens_out
     mass_out = mass if mass_out is None else mass_out
     pos_out = pos if pos_out is None else pos_out
-    b = _batch(side[2], table, lens, None, seqs, 1, max_len, device)
+    b = _batch(side[2], table, lens, None, seqs, 1, max_len, dev)
     lib = N.load()
     need = lib.splitzip_kv4_evict_work_bytes(c, b, budget)
     if need == 0:
         raise N.SplitZipError(N.E_INVALID, "splitzip_kv4_evict_work_bytes")
-    if work is None:
-        work = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        N._device_buffer(work, "work", need)
-        if work.device != device:
-            raise ValueError(f"work must be on {device}")
+    work = _work(work, need, dev)
     rc = lib.splitzip_kv4_evict(
-        c, b, budget, sinks, recent, _tensor(next_pos, "next_pos", torch.int32, (seqs,), device),
-        _tensor(mass, "mass", torch.float32, side, device), _tensor(pos, "pos", torch.int32, side, device),
-        _tensor(lens_out, "lens_out", torch.int32, (seqs,), device),
-        _tensor(mass_out, "mass_out", torch.float32, side, device),
-        _tensor(pos_out, "pos_out", torch.int32, side, device), work.data_ptr(), N._nbytes(work),
-        _status(status, device), _stream(device))
+        c, b, budget, sinks, recent, _tensor(next_pos, "next_pos", torch.int32, (seqs,), dev),
+        _tensor(mass, "mass", torch.float32, side, dev), _tensor(pos, "pos", torch.int32, side, dev),
+        _tensor(lens_out, "lens_out", torch.int32, (seqs,), dev),
+        _tensor(mass_out, "mass_out", torch.float32, side, dev),
+        _tensor(pos_out, "pos_out", torch.int32, side, dev), work.data_ptr(), N._nbytes(work),
+        _status(status, dev), _stream(dev))
     _check(rc, "splitzip_kv4_evict")
     return lens_out, mass_out, pos_out
