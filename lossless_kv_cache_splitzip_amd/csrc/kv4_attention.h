@@ -218,7 +218,8 @@ __device__ inline T get(const uint8_t* p) {
 // Lane (i, j)'s bytes of the 16 slots at `t` (in a page, uniform) of `base`.
 // kOnce: no other workgroup reads these codes (non-temporal: 96 -> 87 us on
 // 374 MB of scattered pages); the scales share their lines with other slots'.
-template <int D, bool kOnce, bool kV = true>
+// kOnceK: nor K's.
+template <int D, bool kOnce, bool kV = true, bool kOnceK = kOnce>
 __device__ inline void load_raw(const uint8_t* base, uint32_t shift, uint32_t t, const LaneAt<D>& at, Raw<D>& r) {
   using L = Layout<D>;
   const uint8_t* k = base + t * L::kCode;
@@ -226,16 +227,16 @@ __device__ inline void load_raw(const uint8_t* base, uint32_t shift, uint32_t t,
   const uint8_t* ks = base + L::k_scales(shift) + t * L::kScale;
   const uint8_t* vs = base + L::v_scales(shift) + t * L::kScale;
   if constexpr (D == 64) {
-    *reinterpret_cast<u32x2*>(r.k) = get<kOnce, u32x2>(k + at.k);
+    *reinterpret_cast<u32x2*>(r.k) = get<kOnceK, u32x2>(k + at.k);
     r.ks = ks[at.ks];
     if constexpr (kV) *reinterpret_cast<u32x2*>(r.v) = get<kOnce, u32x2>(v + at.v);
   } else if constexpr (D == 128) {
-    *reinterpret_cast<u32x4*>(r.k) = get<kOnce, u32x4>(k + at.k);
+    *reinterpret_cast<u32x4*>(r.k) = get<kOnceK, u32x4>(k + at.k);
     r.ks = ks[at.ks];
     if constexpr (kV) *reinterpret_cast<u32x4*>(r.v) = get<kOnce, u32x4>(v + at.v);
   } else {
-    *reinterpret_cast<u32x4*>(r.k) = get<kOnce, u32x4>(k + at.k);
-    *reinterpret_cast<u32x4*>(r.k + 4) = get<kOnce, u32x4>(k + at.k + 64);
+    *reinterpret_cast<u32x4*>(r.k) = get<kOnceK, u32x4>(k + at.k);
+    *reinterpret_cast<u32x4*>(r.k + 4) = get<kOnceK, u32x4>(k + at.k + 64);
     r.ks = ks[at.ks] | (uint32_t)ks[at.ks + 4] << 8;
     if constexpr (kV) {
       *reinterpret_cast<u32x4*>(r.v) = get<kOnce, u32x4>(v + at.v);
@@ -353,7 +354,9 @@ __device__ inline void store2(uint8_t* out, uint64_t elem, bool half, float a, f
 // One workgroup: the slots of one piece, 16 kRows query rows of one KV head of
 // one sequence.  Each wave takes every 4th tile of 32 slots with a softmax of
 // its own; the four are joined through LDS.
-template <int D, int kRows, bool kHalf>
+// kAgain: the weights' kernel reads K again, so the caches are to keep it (32 x
+// 8192 slots: 79 -> 77 us, 8 x 32768: 64 -> 62).
+template <int D, int kRows, bool kHalf, bool kAgain>
 __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : kRows == 1 || D == 64 ? 3 : 2) void kv4_attend_kernel(AttArgs g) {
   constexpr int kSteps = D / 32;
   __shared__ float sh_o[4][16][D + 4];
@@ -407,7 +410,7 @@ __global__ __launch_bounds__(kAttThreads, D == 256 ? 1 : kRows == 1 || D == 64 ?
     for (int h = 0; h < 2; ++h) {
       const uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)pages, (int)(2 * (it & 31) + h)) & ~kBadPage;
       const uint8_t* base = a.pages + ((uint64_t)p * a.n_heads + head) * a.page_bytes;
-      load_raw<D, kRows == 1>(base, a.page_shift, __builtin_amdgcn_readfirstlane(slot_of(it, h)) & in_page, lane_at, r[h]);
+      load_raw<D, kRows == 1, true, kRows == 1 && !kAgain>(base, a.page_shift, __builtin_amdgcn_readfirstlane(slot_of(it, h)) & in_page, lane_at, r[h]);
     }
   };
   auto compute = [&](uint32_t it, Raw<D> (&cur)[2]) {
@@ -1149,9 +1152,12 @@ int attend(const Plan& p, const splitzip_kv4_batch* b, const AttArgs& g, hipStre
   // no row at all: only the weights' arrays are copied
   if (p.rows_max > 0 && p.tile_rows >= 64) kv4_extend_kernel<D, kHalf><<<dim3(g.a.n_heads, p.row_tiles, p.grid), kAttThreads, 0, stream>>>(g);
   if constexpr (D != 256) {
-    if (p.rows_max > 0 && p.tile_rows == 32) kv4_attend_kernel<D, 2, kHalf><<<grid, kAttThreads, 0, stream>>>(g);
+    if (p.rows_max > 0 && p.tile_rows == 32) kv4_attend_kernel<D, 2, kHalf, false><<<grid, kAttThreads, 0, stream>>>(g);
   }
-  if (p.rows_max > 0 && p.tile_rows == 16) kv4_attend_kernel<D, 1, kHalf><<<grid, kAttThreads, 0, stream>>>(g);
+  if (p.rows_max > 0 && p.tile_rows == 16) {
+    if (g.mass_out) kv4_attend_kernel<D, 1, kHalf, true><<<grid, kAttThreads, 0, stream>>>(g);
+    else kv4_attend_kernel<D, 1, kHalf, false><<<grid, kAttThreads, 0, stream>>>(g);
+  }
   if (hipGetLastError() != hipSuccess) return SPLITZIP_E_HIP;
   if (p.rows_max > 0 && p.grid > b->n_seqs) {
     // a workgroup a row until those fill the GPU
