@@ -10,7 +10,7 @@
 //
 // Up to 16384 slots a head is one workgroup's, which keeps the keys in
 // registers (kv4_evict_short_kernel); beyond that a head's slots are shared by
-// workgroups of 4096, in six launches that exchange counts.  A moved token
+// workgroups of 4096 each, in six launches that exchange counts.  A moved token
 // costs more than its bytes: its V codes lie in 4-byte pieces between those of
 // 3 neighbours, so whole sectors come and go, about 1.1 KB a token.
 #ifndef SPLITZIP_KV4_EVICT_H
@@ -22,9 +22,12 @@
 
 namespace kv4 {
 
-constexpr uint32_t kEvThreads = 1024, kMoveThreads = 256;
-constexpr uint32_t kChunk = 4 * kEvThreads;  // slots of a workgroup's round: 4 a thread, of one page
-constexpr uint32_t kShortLen = 4 * kChunk;   // one workgroup a head up to this length
+constexpr uint32_t kMoveThreads = 256;
+constexpr uint32_t kShortLen = 16384;  // one workgroup a head up to this length
+// Beyond: 8 consecutive slots a thread (3 x 131,072 slots, 8 heads: 1024 threads of
+// 4 slots 111 us, 512 of 8 106, 256 of 16 120, 1024 of 8 117).
+constexpr uint32_t kEvThreads = 512, kEvRun = 2;
+constexpr uint32_t kChunk = 4 * kEvRun * kEvThreads;
 constexpr uint32_t kBins = 2048;
 constexpr uint32_t kListed = 1024;           // moves that the short form keeps in LDS and does itself
 
@@ -41,6 +44,7 @@ struct EvArgs {
   uint32_t* holes;    // [seq][head][max_moves]
   uint32_t* movers;
   uint32_t* bins;     // [seq][head][3][kBins]
+  u32x4* found;       // [seq][head][3]: what the digits up to each say: key, how many of its equals stay, equals
   uint32_t* counts;   // [seq][head][chunks][4]: keys above / equal to the last kept, below / beyond the new length
 };
 
@@ -171,7 +175,7 @@ struct Ranks {
   uint32_t equal, hole, mover;  // before these slots
 };
 
-template <uint32_t kThreads, int kRun>
+template <uint32_t kThreads, uint32_t kRun>
 __device__ inline void place_run(const EvArgs& e, const Unit& u, const Four (&f)[kRun], uint32_t slot, uint32_t key,
                                  uint32_t ties, bool all_equal_stay, Ranks& r, uint32_t* holes, uint32_t* movers,
                                  Scan<kThreads>& scan) {
@@ -179,7 +183,7 @@ __device__ inline void place_run(const EvArgs& e, const Unit& u, const Four (&f)
   if (!all_equal_stay) {
     uint32_t n = 0;
 #pragma unroll
-    for (int c = 0; c < kRun; ++c)
+    for (uint32_t c = 0; c < kRun; ++c)
 #pragma unroll
       for (int k = 0; k < 4; ++k) n += f[c].in[k] && f[c].key[k] == key;
     rank = r.equal + scan(n, all);
@@ -187,7 +191,7 @@ __device__ inline void place_run(const EvArgs& e, const Unit& u, const Four (&f)
   }
   uint32_t keep = 0, hole = 0, mover = 0;  // keep: a bit a slot
 #pragma unroll
-  for (int c = 0; c < kRun; ++c)
+  for (uint32_t c = 0; c < kRun; ++c)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t at = slot + 4 * c + k;
@@ -205,7 +209,7 @@ __device__ inline void place_run(const EvArgs& e, const Unit& u, const Four (&f)
   r.mover += all >> 16;
   if (hole | mover) {
 #pragma unroll
-    for (int c = 0; c < kRun; ++c)
+    for (uint32_t c = 0; c < kRun; ++c)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t at = slot + 4 * c + k;
@@ -216,7 +220,7 @@ __device__ inline void place_run(const EvArgs& e, const Unit& u, const Four (&f)
   }
   if (e.mass_out == e.mass && e.pos_out == e.pos) return;
 #pragma unroll
-  for (int c = 0; c < kRun; ++c) {
+  for (uint32_t c = 0; c < kRun; ++c) {
     if (f[c].at == kNowhere) continue;
     if ((keep >> (4 * c) & 15u) == 15u && slot + 4 * c + 4 <= u.left) {  // the usual case: whole words
       if (e.mass_out != e.mass) *reinterpret_cast<f32x4*>(e.mass_out + f[c].at) = f[c].mass;
@@ -293,7 +297,7 @@ __device__ inline void move_some(const EvArgs& e, uint32_t b, uint32_t head, con
 
 // One workgroup a head, 4 kRun consecutive slots a thread, keys in registers.
 // kFused: at most kListed moves, done here too.
-template <int D, uint32_t kThreads, int kRun, bool kFused>
+template <int D, uint32_t kThreads, uint32_t kRun, bool kFused>
 __global__ __launch_bounds__(kThreads) void kv4_evict_short_kernel(EvArgs e) {
   __shared__ uint32_t hist[kBins], sh[2][kThreads / 64];
   __shared__ uint32_t list[2][kFused ? kListed : 1];
@@ -307,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void kv4_evict_short_kernel(EvArgs e) {
   for (uint32_t k = 0; k < kBins; k += kThreads) hist[k + tid] = 0;
   Four f[kRun];
 #pragma unroll
-  for (int c = 0; c < kRun; ++c) load_four(e, u, 4 * (kRun * tid + c), f[c]);
+  for (uint32_t c = 0; c < kRun; ++c) load_four(e, u, 4 * (kRun * tid + c), f[c]);
   uint32_t key = 0, ties = 0, equal = 0;
   if (u.len > u.left) {
     uint32_t want = u.left;
@@ -315,7 +319,7 @@ __global__ __launch_bounds__(kThreads) void kv4_evict_short_kernel(EvArgs e) {
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
 #pragma unroll
-      for (int c = 0; c < kRun; ++c) count_four(f[c], pass, key, hist);
+      for (uint32_t c = 0; c < kRun; ++c) count_four(f[c], pass, key, hist);
       __syncthreads();
       const Chosen d = choose<true>(hist, want, scan, &chosen[pass]);
       key |= d.digit << shift_of(pass);
@@ -342,19 +346,15 @@ __global__ __launch_bounds__(256) void kv4_evict_zero_kernel(u32x4* p, uint64_t 
   if (i < n) p[i] = u32x4{0, 0, 0, 0};
 }
 
-// The key found by the passes before `pass`, from their counts.
-__device__ inline uint32_t key_before(const EvArgs& e, const Unit& u, int pass, Scan<kEvThreads>& scan, Chosen out[3],
-                                      uint32_t& ties, uint32_t& equal) {
-  uint32_t key = 0;
-  ties = u.left;
-  equal = 0;
-  for (int p = 0; p < pass; ++p) {
-    const Chosen d = choose<false>(e.bins + ((uint64_t)u.at * 3 + p) * kBins, ties, scan, &out[p]);
-    key |= d.digit << shift_of(p);
-    ties = d.rest;
-    equal = d.equal;
-  }
-  return key;
+// The key that the passes before `pass` (1, 2, 3) found: what an earlier launch
+// wrote down and the last pass's counts.
+__device__ inline Chosen key_before(const EvArgs& e, const Unit& u, int pass, Scan<kEvThreads>& scan, Chosen* out) {
+  u32x4* found = e.found + (uint64_t)u.at * 3;
+  const u32x4 old = pass == 1 ? u32x4{0, u.left, 0, 0} : found[pass - 2];
+  const Chosen d = choose<false>(e.bins + ((uint64_t)u.at * 3 + pass - 1) * kBins, old[1], scan, out);
+  const uint32_t key = old[0] | d.digit << shift_of(pass - 1);
+  if (blockIdx.x == 0 && threadIdx.x == 0) found[pass - 1] = u32x4{key, d.rest, d.equal, 0};
+  return Chosen{key, d.rest, d.equal};
 }
 
 // Long heads, pass 0, 1, 2: a chunk's digits into the head's counts.  Pass 3:
@@ -362,36 +362,40 @@ __device__ inline uint32_t key_before(const EvArgs& e, const Unit& u, int pass, 
 template <int kPass>
 __global__ __launch_bounds__(kEvThreads) void kv4_evict_count_kernel(EvArgs e) {
   __shared__ uint32_t hist[kBins], sh[2][kEvThreads / 64];
-  __shared__ Chosen chosen[3];
+  __shared__ Chosen chosen;
   Scan<kEvThreads> scan = {sh, 0};
-  const uint32_t tid = threadIdx.x, slot = blockIdx.x * kChunk + 4 * tid;
+  const uint32_t tid = threadIdx.x, slot = blockIdx.x * kChunk + 4 * kEvRun * tid;
   const Unit u = unit_of(e, blockIdx.y, blockIdx.z);
   if (kPass == 0 && !u.ok && tid == 0) corrupt(e.a.status);
   if (u.len <= u.left || blockIdx.x * kChunk >= u.len) return;
-  Four f;
-  load_four(e, u, slot, f);
-  uint32_t ties, equal;
-  const uint32_t key = key_before(e, u, kPass, scan, chosen, ties, equal);
+  Four f[kEvRun];
+#pragma unroll
+  for (uint32_t c = 0; c < kEvRun; ++c) load_four(e, u, slot + 4 * c, f[c]);
+  uint32_t key = 0;
+  if constexpr (kPass > 0) key = key_before(e, u, kPass, scan, &chosen).digit;
   if constexpr (kPass < 3) {
-    hist[tid] = 0;
-    hist[tid + kEvThreads] = 0;
+#pragma unroll
+    for (uint32_t n = 0; n < kBins; n += kEvThreads) hist[n + tid] = 0;
     __syncthreads();
-    count_four(f, kPass, key, hist);
+#pragma unroll
+    for (uint32_t c = 0; c < kEvRun; ++c) count_four(f[c], kPass, key, hist);
     __syncthreads();
     uint32_t* to = e.bins + ((uint64_t)u.at * 3 + kPass) * kBins;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t n = hist[tid + k * kEvThreads];
-      if (n) __hip_atomic_fetch_add(&to[tid + k * kEvThreads], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (uint32_t k = 0; k < kBins; k += kEvThreads) {
+      const uint32_t n = hist[tid + k];
+      if (n) __hip_atomic_fetch_add(&to[tid + k], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   } else {
     uint32_t low = 0, high = 0, all_low, all_high;  // above | equal << 16
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t n = f.in[k] ? (f.key[k] > key ? 1u : f.key[k] == key ? 1u << 16 : 0u) : 0u;
-      if (slot + k < u.left) low += n;
-      else high += n;
-    }
+    for (uint32_t c = 0; c < kEvRun; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t n = f[c].in[k] ? (f[c].key[k] > key ? 1u : f[c].key[k] == key ? 1u << 16 : 0u) : 0u;
+        if (slot + 4 * c + k < u.left) low += n;
+        else high += n;
+      }
     scan(low, all_low);
     scan(high, all_high);
     if (tid == 0)
@@ -404,20 +408,24 @@ __global__ __launch_bounds__(kEvThreads) void kv4_evict_count_kernel(EvArgs e) {
 // counts of the chunks before it.
 __global__ __launch_bounds__(kEvThreads) void kv4_evict_list_kernel(EvArgs e) {
   __shared__ uint32_t sh[2][kEvThreads / 64];
-  __shared__ Chosen chosen[3];
   Scan<kEvThreads> scan = {sh, 0};
-  const uint32_t tid = threadIdx.x, chunk = blockIdx.x, slot = chunk * kChunk + 4 * tid;
+  const uint32_t tid = threadIdx.x, chunk = blockIdx.x, slot = chunk * kChunk + 4 * kEvRun * tid;
   const Unit u = unit_of(e, blockIdx.y, blockIdx.z);
   if (chunk == 0 && tid == 0 && u.len <= u.left) e.n_moves[u.at] = 0;
   if (chunk * kChunk >= u.len) return;
-  Four f[1];
-  load_four(e, u, slot, f[0]);
-  uint32_t key = 0, ties = 0, equal = 0;
+  Four f[kEvRun];
+#pragma unroll
+  for (uint32_t c = 0; c < kEvRun; ++c) load_four(e, u, slot + 4 * c, f[c]);
+  uint32_t key = 0, ties = 0;
+  bool all_stay = true;  // all of the last kept key's equals
   Ranks r = {0, 0, 0};
   if (u.len > u.left) {
-    key = key_before(e, u, 3, scan, chosen, ties, equal);
+    const u32x4 found = e.found[(uint64_t)u.at * 3 + 2];
+    key = found[0];
+    ties = found[1];
+    all_stay = ties == found[2];
     const u32x4* counts = reinterpret_cast<const u32x4*>(e.counts + (uint64_t)u.at * e.chunks * 4);
-    // equal keys before each earlier chunk decide how many of its own stay: scanned 1024 chunks at a time
+    // equal keys before each earlier chunk decide how many of its own stay: scanned a chunk a thread at a time
     for (uint32_t c0 = 0; c0 < chunk; c0 += kEvThreads) {
       const uint32_t c = c0 + tid;
       const u32x4 n = c < chunk ? counts[c] : u32x4{0, 0, 0, 0};
@@ -432,7 +440,7 @@ __global__ __launch_bounds__(kEvThreads) void kv4_evict_list_kernel(EvArgs e) {
       r.mover += all;
     }
   }
-  place_run(e, u, f, slot, key, ties, u.len <= u.left, r, e.holes + (uint64_t)u.at * e.max_moves,
+  place_run(e, u, f, slot, key, ties, all_stay, r, e.holes + (uint64_t)u.at * e.max_moves,
              e.movers + (uint64_t)u.at * e.max_moves, scan);
   // the last chunk knows how many there are
   if (u.len > u.left && (chunk + 1) * kChunk >= u.len && tid == 0) e.n_moves[u.at] = r.mover;
@@ -462,7 +470,7 @@ __global__ __launch_bounds__(256) void kv4_lens_kernel(EvArgs e) {
 }
 
 struct EvPlan {
-  uint64_t holes, movers, bins, counts, bytes;
+  uint64_t holes, movers, bins, counts, found, bytes;
   uint32_t max_moves, chunks;
 };
 
@@ -476,7 +484,8 @@ inline EvPlan ev_plan(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, 
   p.movers = p.holes + up(units * p.max_moves * 4, 256);
   p.bins = p.movers + up(units * p.max_moves * 4, 256);
   p.counts = p.bins + (p.chunks ? units * 3 * kBins * 4 : 0);
-  p.bytes = p.counts + up(units * p.chunks * 16, 256);
+  p.found = p.counts + up(units * p.chunks * 16, 256);
+  p.bytes = p.found + (p.chunks ? units * 48 : 0);
   if (p.bytes < 256) p.bytes = 256;
   return p;
 }
@@ -565,6 +574,7 @@ int splitzip_kv4_evict(const splitzip_kv4_cache* cache, const splitzip_kv4_batch
   e.movers = reinterpret_cast<uint32_t*>(w + p.movers);
   e.bins = reinterpret_cast<uint32_t*>(w + p.bins);
   e.counts = reinterpret_cast<uint32_t*>(w + p.counts);
+  e.found = reinterpret_cast<u32x4*>(w + p.found);
   if (cache->head_dim == 64) return evict<64>(e, p, stream);
   return cache->head_dim == 128 ? evict<128>(e, p, stream) : evict<256>(e, p, stream);
 }
