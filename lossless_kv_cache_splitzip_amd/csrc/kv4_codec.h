@@ -20,6 +20,10 @@ namespace kv4 {
 
 constexpr int kRowThreads = 256;
 constexpr uint64_t kEnoughWaves = 4096;  // 1024 to 8192 measure alike
+// Where 4 rows take at most so many lanes, a wave has 8 or 16 rows (177,803 rows
+// of one head, append and read: 64 channels 56 -> 37 us, 128 60 -> 54; at 256
+// lanes 95 -> 90 for BF16, but 50 -> 52.6 for 48,756 rows of E5M2).
+constexpr uint32_t kNarrowLanes = 128;
 
 struct RowArgs {
   Batch a;
@@ -28,7 +32,8 @@ struct RowArgs {
   uint8_t* k_out;
   uint8_t* v_out;
   uint64_t k_row, k_head, v_row, v_head;  // strides in elements
-  uint32_t chunks, per_wave, waves;       // of 4 rows: pieces of 64 lanes, how many a wave does, waves
+  uint32_t rows, width;                   // a wave's packed rows: 4, 8 or 16; lanes that 4 rows take
+  uint32_t chunks, per_wave, waves;       // of those rows: pieces of 64 lanes, how many a wave does, waves
   const int32_t* positions;
   float* mass;
   int32_t* pos;
@@ -115,34 +120,34 @@ __device__ inline uint32_t encode8(u32x4 q, uint32_t& scale, bool& odd) {
   return c;
 }
 
-// A wave of the row kernels has 4 packed rows and some of their heads: lanes
-// run over the rows first, then over 8 channels each, then over the heads, in
-// chunks of 64 lanes.  What belongs to the rows is looked up once.  Rows that
-// start at a multiple of 4 slots fill whole words of the V codes, others two
-// parts of them.  The grid goes by the packed rows alone, however ragged the
-// batch.
+// A wave of the row kernels has 4 packed rows and some of their heads, or where
+// heads are few 8 or 16 rows with all of them: lanes run over 4 rows first, then
+// over 8 channels each, the heads, and the next 4 rows, in chunks of 64 lanes.
+// What belongs to the rows is looked up once, by the lanes of their numbers.
+// Rows that start at a multiple of 4 slots fill whole words of the V codes,
+// others two parts of them.  The grid goes by the packed rows alone, however
+// ragged the batch.
 struct Place {
-  uint32_t row0;      // of the wave's 4
-  uint32_t row;       // this lane's
+  uint32_t row;       // packed
   uint32_t slot, t;   // its slot, in the sequence and in the page
-  uint32_t page;
-  uint8_t* base;      // the page's bytes
-  bool on;            // false: no slot, or a page number outside the pool
+  uint32_t page;      // kBadPage: no slot, or a page number outside the pool
 };
 
 // The sequence of a packed row: the first whose rows end behind it.  64
 // sequences are looked at in one round of loads, with one vote a row.
-__device__ inline uint32_t seq_of_row(const Batch& a, uint32_t row0, uint32_t t) {
+__device__ inline uint32_t seq_of_row(const Batch& a, uint32_t row0, uint32_t t, uint32_t rows) {
   if (!a.cu) return row0 + t;
   const uint32_t lane = threadIdx.x & 63;
   uint32_t seq = a.n_seqs;
   for (uint32_t b = 0; b < a.n_seqs; b += 64) {
     const int32_t end = b + lane < a.n_seqs ? a.cu[b + lane + 1] : 0;
     uint32_t mine = a.n_seqs;
+    for (uint32_t g = 0; g < rows; g += 4) {
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-      const uint64_t hit = __ballot(b + lane < a.n_seqs && end > (int32_t)(row0 + k));
-      if (k == t && hit) mine = b + (uint32_t)__builtin_ctzll(hit);
+      for (uint32_t k = 0; k < 4; ++k) {
+        const uint64_t hit = __ballot(b + lane < a.n_seqs && end > (int32_t)(row0 + g + k));
+        if (g + k == t && hit) mine = b + (uint32_t)__builtin_ctzll(hit);
+      }
     }
     if (mine < seq) seq = mine;
     if (__all(seq < a.n_seqs)) break;
@@ -150,34 +155,38 @@ __device__ inline uint32_t seq_of_row(const Batch& a, uint32_t row0, uint32_t t)
   return seq;
 }
 
-__device__ inline Place place_of(const Batch& a, uint32_t row0) {
-  Place p;
-  p.row0 = row0;
-  p.row = row0 + (threadIdx.x & 3);
-  p.on = false;
-  const uint32_t b = seq_of_row(a, row0, threadIdx.x & 3);
+__device__ inline Place place_of(const Batch& a, uint32_t row0, uint32_t rows) {
+  const uint32_t t = threadIdx.x & (rows - 1);
+  Place p = {row0 + t, 0, 0, kBadPage};
+  const uint32_t b = seq_of_row(a, row0, t, rows);
   if (p.row >= a.n_rows || b >= a.n_seqs) return p;
   const Seq s = seq_of(a, b);
   if (!s.ok || s.rows > s.len || p.row < (uint32_t)s.row0 || p.row >= (uint32_t)(s.row0 + s.rows)) return p;
   p.slot = (uint32_t)(s.len - s.rows) + (p.row - (uint32_t)s.row0);
-  p.page = page_of(a, b, p.slot >> a.page_shift);
-  p.on = p.page != kBadPage;
-  if (!p.on) return p;
   p.t = p.slot & ((1u << a.page_shift) - 1);
-  p.base = a.pages + (uint64_t)p.page * a.n_heads * a.page_bytes;
+  p.page = page_of(a, b, p.slot >> a.page_shift);
   return p;
 }
 
-// A lane's head and 8 channels (8u ..) in a chunk; `in`: there are such.
-template <int D>
+// A lane's 4 rows (of the wave's), head and 8 channels (8u ..) in a chunk;
+// `in`: there are such.
+template <int D, bool kNarrow>
 struct Col {
-  uint32_t head, u;
+  uint32_t group = 0, head, u;
   bool in;
-  __device__ Col(const Batch& a, uint32_t chunk) {
-    const uint32_t col = chunk * 64 + (threadIdx.x & 63);
+  __device__ Col(const RowArgs& r, uint32_t chunk) {
+    uint32_t col = chunk * 64 + (threadIdx.x & 63);
+    if constexpr (kNarrow) {
+      group = (col >= r.width ? 1 : 0) + (col >= 2 * r.width ? 1 : 0) + (col >= 3 * r.width ? 1 : 0);
+      col -= group * r.width;
+    }
     head = col / (D / 2);
     u = col % (D / 2) >> 2;
-    in = head < a.n_heads;
+    in = head < r.a.n_heads && (!kNarrow || 4 * group < r.rows);
+  }
+  // What the lane of this lane's row holds: all 64 lanes ask.
+  __device__ uint32_t of_row(const RowArgs& r, uint32_t v) const {
+    return kNarrow ? (uint32_t)__shfl((int)v, (int)(4 * group + (threadIdx.x & 3))) : v;
   }
 };
 
@@ -193,20 +202,21 @@ __device__ inline void report_bad(const Batch& a) {
   }
 }
 
-template <int D, int T>
+template <int D, int T, bool kNarrow>
 __global__ __launch_bounds__(kRowThreads) void kv4_append_kernel(RowArgs r) {
   using L = Layout<D>;
   const Batch& a = r.a;
   report_bad(a);
   const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6));
-  const uint32_t row0 = wave / r.waves * 4, first = wave % r.waves * r.per_wave, end = min(first + r.per_wave, r.chunks);
+  const uint32_t rows = kNarrow ? r.rows : 4;
+  const uint32_t row0 = wave / r.waves * rows, first = wave % r.waves * r.per_wave, end = min(first + r.per_wave, r.chunks);
   if (row0 >= a.n_rows) return;
   Eight<T> kq[kTogetherRows], vq[kTogetherRows];
   auto load = [&](uint32_t c) {  // rows that turn out to have no slot, too
-    const uint64_t row = row0 + (threadIdx.x & 3);
 #pragma unroll
     for (uint32_t n = 0; n < kTogetherRows; ++n) {
-      const Col<D> col(a, c + n);
+      const Col<D, kNarrow> col(r, c + n);
+      const uint64_t row = row0 + 4 * col.group + (threadIdx.x & 3);
       kq[n] = vq[n] = Eight<T>{};
       if (c + n < end && col.in && row < a.n_rows) {
         kq[n] = load8<T>(r.k, row * r.k_row + col.head * r.k_head + 8 * col.u);
@@ -215,40 +225,42 @@ __global__ __launch_bounds__(kRowThreads) void kv4_append_kernel(RowArgs r) {
     }
   };
   load(first);
-  const Place p = place_of(a, row0);
+  const Place p = place_of(a, row0, rows);
   const uint32_t sh = a.page_shift;
-  const int32_t position = p.on ? (r.positions && r.pos ? r.positions[p.row] : (int32_t)p.slot) : 0;
+  const int32_t position = r.positions && r.pos && p.page != kBadPage ? r.positions[p.row] : (int32_t)p.slot;
   bool odd = false;
   for (uint32_t c = first; c < end; c += kTogetherRows) {
     if (c > first) load(c);
 #pragma unroll
     for (uint32_t n = 0; n < kTogetherRows; ++n) {
       if (c + n >= end) break;
-      const Col<D> col(a, c + n);
+      const Col<D, kNarrow> col(r, c + n);
+      const uint32_t page = col.of_row(r, p.page), t = col.of_row(r, p.t);
+      const int32_t at_position = (int32_t)col.of_row(r, (uint32_t)position);
       uint32_t ks, vs;
       bool k_odd = false, v_odd = false;
       const uint32_t kc = encode8<T>(as16<T>(kq[n]), ks, k_odd), vc = encode8<T>(as16<T>(vq[n]), vs, v_odd);
-      if (!p.on || !col.in) continue;
+      if (page == kBadPage || !col.in) continue;
       odd |= k_odd | v_odd;
-      uint8_t* base = p.base + col.head * a.page_bytes;
-      *reinterpret_cast<uint32_t*>(base + p.t * L::kCode + 4 * col.u) = kc;
+      uint8_t* base = a.pages + (uint64_t)page * a.n_heads * a.page_bytes + col.head * a.page_bytes;
+      *reinterpret_cast<uint32_t*>(base + t * L::kCode + 4 * col.u) = kc;
       uint8_t* v = base + L::v_codes(sh);
       if constexpr (D == 64) {  // 8 channels are two pieces of 2 bytes
-        *reinterpret_cast<uint16_t*>(v + L::v_piece(p.t, 2 * col.u)) = (uint16_t)vc;
-        *reinterpret_cast<uint16_t*>(v + L::v_piece(p.t, 2 * col.u + 1)) = (uint16_t)(vc >> 16);
+        *reinterpret_cast<uint16_t*>(v + L::v_piece(t, 2 * col.u)) = (uint16_t)vc;
+        *reinterpret_cast<uint16_t*>(v + L::v_piece(t, 2 * col.u + 1)) = (uint16_t)(vc >> 16);
       } else if constexpr (D == 128) {
-        *reinterpret_cast<uint32_t*>(v + L::v_piece(p.t, col.u)) = vc;
+        *reinterpret_cast<uint32_t*>(v + L::v_piece(t, col.u)) = vc;
       } else {  // half a piece of 8 bytes
-        *reinterpret_cast<uint32_t*>(v + L::v_piece(p.t, col.u >> 1) + 4 * (col.u & 1)) = vc;
+        *reinterpret_cast<uint32_t*>(v + L::v_piece(t, col.u >> 1) + 4 * (col.u & 1)) = vc;
       }
       if ((col.u & 3) == 0) {
-        base[L::k_scales(sh) + p.t * L::kScale + col.u / 4] = (uint8_t)ks;
-        base[L::v_scales(sh) + L::v_scale(p.t, col.u / 4)] = (uint8_t)vs;
+        base[L::k_scales(sh) + t * L::kScale + col.u / 4] = (uint8_t)ks;
+        base[L::v_scales(sh) + L::v_scale(t, col.u / 4)] = (uint8_t)vs;
       }
       if (col.u == 0) {
-        const uint64_t at = (((uint64_t)p.page * a.n_heads + col.head) << sh) + p.t;
+        const uint64_t at = (((uint64_t)page * a.n_heads + col.head) << sh) + t;
         if (r.mass) r.mass[at] = 0.0f;
-        if (r.pos) r.pos[at] = position;
+        if (r.pos) r.pos[at] = at_position;
       }
     }
   }
@@ -286,47 +298,52 @@ __device__ inline u32x4 decode8(uint32_t c, uint32_t scale) {
 // The rows are not read again here: past the caches (24,348 rows: 45.8 -> 29.4 us between other work).
 __device__ inline void put16(uint8_t* p, u32x4 v) { __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p)); }
 
-template <int D, int T>
+template <int D, int T, bool kNarrow>
 __global__ __launch_bounds__(kRowThreads) void kv4_read_kernel(RowArgs r) {
   using L = Layout<D>;
   const Batch& a = r.a;
   report_bad(a);
   const uint32_t wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6));
-  const uint32_t row0 = wave / r.waves * 4, first = wave % r.waves * r.per_wave, end = min(first + r.per_wave, r.chunks);
+  const uint32_t rows = kNarrow ? r.rows : 4;
+  const uint32_t row0 = wave / r.waves * rows, first = wave % r.waves * r.per_wave, end = min(first + r.per_wave, r.chunks);
   if (row0 >= a.n_rows) return;
-  const Place p = place_of(a, row0);
-  if (!p.on) return;
+  const Place p = place_of(a, row0, rows);
+  if (!__any(p.page != kBadPage)) return;
   const uint32_t sh = a.page_shift;
   for (uint32_t c = first; c < end; c += kTogetherRows) {
     uint32_t kc[kTogetherRows], vc[kTogetherRows], ks[kTogetherRows], vs[kTogetherRows];
+    bool on[kTogetherRows];
 #pragma unroll
     for (uint32_t n = 0; n < kTogetherRows; ++n) {
-      const Col<D> col(a, c + n);
+      const Col<D, kNarrow> col(r, c + n);
+      const uint32_t page = col.of_row(r, p.page), t = col.of_row(r, p.t);
       kc[n] = vc[n] = ks[n] = vs[n] = 0;
-      if (c + n >= end || !col.in) continue;
-      const uint8_t* base = p.base + col.head * a.page_bytes;
+      on[n] = c + n < end && col.in && page != kBadPage;
+      if (!on[n]) continue;
+      const uint8_t* base = a.pages + (uint64_t)page * a.n_heads * a.page_bytes + col.head * a.page_bytes;
       if (r.k_out) {
-        kc[n] = *reinterpret_cast<const uint32_t*>(base + p.t * L::kCode + 4 * col.u);
-        ks[n] = base[L::k_scales(sh) + p.t * L::kScale + col.u / 4];
+        kc[n] = *reinterpret_cast<const uint32_t*>(base + t * L::kCode + 4 * col.u);
+        ks[n] = base[L::k_scales(sh) + t * L::kScale + col.u / 4];
       }
       if (r.v_out) {
         const uint8_t* v = base + L::v_codes(sh);
         if constexpr (D == 64) {
-          vc[n] = *reinterpret_cast<const uint16_t*>(v + L::v_piece(p.t, 2 * col.u)) |
-                  (uint32_t) * reinterpret_cast<const uint16_t*>(v + L::v_piece(p.t, 2 * col.u + 1)) << 16;
+          vc[n] = *reinterpret_cast<const uint16_t*>(v + L::v_piece(t, 2 * col.u)) |
+                  (uint32_t) * reinterpret_cast<const uint16_t*>(v + L::v_piece(t, 2 * col.u + 1)) << 16;
         } else if constexpr (D == 128) {
-          vc[n] = *reinterpret_cast<const uint32_t*>(v + L::v_piece(p.t, col.u));
+          vc[n] = *reinterpret_cast<const uint32_t*>(v + L::v_piece(t, col.u));
         } else {
-          vc[n] = *reinterpret_cast<const uint32_t*>(v + L::v_piece(p.t, col.u >> 1) + 4 * (col.u & 1));
+          vc[n] = *reinterpret_cast<const uint32_t*>(v + L::v_piece(t, col.u >> 1) + 4 * (col.u & 1));
         }
-        vs[n] = base[L::v_scales(sh) + L::v_scale(p.t, col.u / 4)];
+        vs[n] = base[L::v_scales(sh) + L::v_scale(t, col.u / 4)];
       }
     }
 #pragma unroll
     for (uint32_t n = 0; n < kTogetherRows; ++n) {
-      const Col<D> col(a, c + n);
-      if (c + n >= end || !col.in) continue;
-      const uint64_t at = ((uint64_t)p.row * a.n_heads + col.head) * D + 8 * col.u;
+      const Col<D, kNarrow> col(r, c + n);
+      if (!on[n]) continue;
+      const uint64_t row = row0 + 4 * col.group + (threadIdx.x & 3);
+      const uint64_t at = (row * a.n_heads + col.head) * D + 8 * col.u;
       if (r.k_out) put16(r.k_out + 2 * at, decode8<T>(kc[n], ks[n]));
       if (r.v_out) put16(r.v_out + 2 * at, decode8<T>(vc[n], vs[n]));
     }
@@ -335,43 +352,51 @@ __global__ __launch_bounds__(kRowThreads) void kv4_read_kernel(RowArgs r) {
 
 // Workgroups for all packed rows (0: more than 2^24); a wave takes one chunk of
 // 64 lanes where rows are few, up to 8 where there are more than enough (21,251
-// rows of 8 heads: append 31 -> 25 us, read 22 -> 20.5).
+// rows of 8 heads: append 31 -> 25 us, read 22 -> 20.5): of 4 rows, or where
+// these have fewer, of 8 or 16.
 inline uint32_t row_blocks(const splitzip_kv4_cache* c, const splitzip_kv4_batch* b, RowArgs* r) {
-  const uint64_t groups = ((uint64_t)b->n_rows + 3) / 4;
-  r->chunks = (c->n_heads * (c->head_dim / 2) + 63) / 64;
+  r->width = c->n_heads * (c->head_dim / 2);
+  r->rows = 4;
+  while (r->rows < 16 && r->rows / 4 * r->width <= kNarrowLanes && b->n_rows >= 2 * r->rows * kEnoughWaves) r->rows *= 2;
+  const uint64_t groups = ((uint64_t)b->n_rows + r->rows - 1) / r->rows;
+  r->chunks = (r->rows / 4 * r->width + 63) / 64;
   const uint64_t all = groups * r->chunks;
   r->per_wave = all >= 8 * kEnoughWaves ? 8 : all >= 4 * kEnoughWaves ? 4 : all >= 2 * kEnoughWaves ? 2 : 1;
+  if (r->rows > 4) r->per_wave = r->chunks;
   r->waves = (r->chunks + r->per_wave - 1) / r->per_wave;
   const uint64_t n = up(groups * r->waves, kRowThreads / 64) / (kRowThreads / 64);
   return n < (1ull << 24) ? (uint32_t)n : 0;
 }
 
-template <template <int, int> class Launch>
-int dispatch(uint32_t dim, int dtype, bool e5m2, const RowArgs& r, dim3 grid, hipStream_t stream) {
-  if (dtype == SPLITZIP_BF16) {
-    if (dim == 64) Launch<64, SPLITZIP_BF16>::go(r, grid, stream);
-    else if (dim == 128) Launch<128, SPLITZIP_BF16>::go(r, grid, stream);
-    else Launch<256, SPLITZIP_BF16>::go(r, grid, stream);
-  } else if (dtype == SPLITZIP_KV4_FP16) {
-    if (dim == 64) Launch<64, SPLITZIP_KV4_FP16>::go(r, grid, stream);
-    else if (dim == 128) Launch<128, SPLITZIP_KV4_FP16>::go(r, grid, stream);
-    else Launch<256, SPLITZIP_KV4_FP16>::go(r, grid, stream);
-  } else if (e5m2) {
-    if (dim == 64) Launch<64, SPLITZIP_FP8_E5M2>::go(r, grid, stream);
-    else if (dim == 128) Launch<128, SPLITZIP_FP8_E5M2>::go(r, grid, stream);
-    else Launch<256, SPLITZIP_FP8_E5M2>::go(r, grid, stream);
-  }
+template <template <int, int, bool> class Launch, int T, bool N>
+void dispatch_dim(uint32_t dim, const RowArgs& r, dim3 grid, hipStream_t stream) {
+  if (dim == 64) Launch<64, T, N>::go(r, grid, stream);
+  else if (dim == 128) Launch<128, T, N>::go(r, grid, stream);
+  else Launch<256, T, N>::go(r, grid, stream);
+}
+
+template <template <int, int, bool> class Launch, bool N>
+int dispatch_type(uint32_t dim, int dtype, const RowArgs& r, dim3 grid, hipStream_t stream) {
+  if (dtype == SPLITZIP_BF16) dispatch_dim<Launch, SPLITZIP_BF16, N>(dim, r, grid, stream);
+  else if (dtype == SPLITZIP_KV4_FP16) dispatch_dim<Launch, SPLITZIP_KV4_FP16, N>(dim, r, grid, stream);
+  else dispatch_dim<Launch, SPLITZIP_FP8_E5M2, N>(dim, r, grid, stream);
   return hipGetLastError() == hipSuccess ? SPLITZIP_OK : SPLITZIP_E_HIP;
 }
 
-template <int D, int T>
+template <template <int, int, bool> class Launch>
+int dispatch(uint32_t dim, int dtype, const RowArgs& r, dim3 grid, hipStream_t stream) {
+  return r.rows > 4 ? dispatch_type<Launch, true>(dim, dtype, r, grid, stream)
+                    : dispatch_type<Launch, false>(dim, dtype, r, grid, stream);
+}
+
+template <int D, int T, bool N>
 struct Append {
-  static void go(const RowArgs& r, dim3 grid, hipStream_t s) { kv4_append_kernel<D, T><<<grid, kRowThreads, 0, s>>>(r); }
+  static void go(const RowArgs& r, dim3 grid, hipStream_t s) { kv4_append_kernel<D, T, N><<<grid, kRowThreads, 0, s>>>(r); }
 };
-template <int D, int T>
+template <int D, int T, bool N>
 struct Read {
   static void go(const RowArgs& r, dim3 grid, hipStream_t s) {
-    if constexpr (T != SPLITZIP_FP8_E5M2) kv4_read_kernel<D, T><<<grid, kRowThreads, 0, s>>>(r);
+    if constexpr (T != SPLITZIP_FP8_E5M2) kv4_read_kernel<D, T, N><<<grid, kRowThreads, 0, s>>>(r);
   }
 };
 
@@ -410,7 +435,7 @@ int splitzip_kv4_append(const splitzip_kv4_cache* cache, const splitzip_kv4_batc
   r.positions = d_positions;
   r.mass = d_mass;
   r.pos = d_pos;
-  return dispatch<Append>(cache->head_dim, dtype, true, r, dim3(x), stream);
+  return dispatch<Append>(cache->head_dim, dtype, r, dim3(x), stream);
 }
 
 int splitzip_kv4_read(const splitzip_kv4_cache* cache, const splitzip_kv4_batch* batch, int dtype, void* d_k,
@@ -426,7 +451,7 @@ int splitzip_kv4_read(const splitzip_kv4_cache* cache, const splitzip_kv4_batch*
   r.a = batch_of(cache, batch, d_status);
   r.k_out = static_cast<uint8_t*>(d_k);
   r.v_out = static_cast<uint8_t*>(d_v);
-  return dispatch<Read>(cache->head_dim, dtype, false, r, dim3(x), stream);
+  return dispatch<Read>(cache->head_dim, dtype, r, dim3(x), stream);
 }
 
 }  // extern "C"

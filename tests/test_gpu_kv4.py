@@ -105,6 +105,53 @@ def test_append_matches_the_layout_and_read_gives_it_back(dim, page, kv, dtype, 
     assert torch.equal(hk.cpu(), kq.to(HF)) and torch.equal(hv.cpu(), vq.to(HF))
 
 
+@pytest.mark.parametrize("dim,kv,dtype,page", [
+    (64, 1, BF, 16), (64, 1, E5, 256), (128, 1, HF, 64), (64, 2, E5, 16), (64, 3, BF, 32), (64, 4, HF, 16), (256, 1, BF, 128)])
+def test_many_rows_of_few_heads_as_in_small_calls(dim, kv, dtype, page):
+    """One call of 70,000 rows and calls of 5000 rows give the same bytes, positions and weights; one sequence has
+    page numbers outside the pool, some have no rows."""
+    before, new = [5, 0, 7, 0, 130, 1, 2], [30001, 1, 0, 38999, 4, 1002, 3]
+    lens = [a + b for a, b in zip(before, new)]
+    print(f"case narrow dim={dim} kv={kv} {dtype} page={page}", flush=True)
+    n_pages = sum(-(-n // page) for n in lens) + 2
+    table = R.table_of(lens, page, n_pages, 17)
+    table[5, 1] = n_pages  # the second page's rows of one sequence have no place
+    total, cu = sum(new), _cu(new)
+    k, v = (_rows(total, kv, dim, torch.float32, s, 2.0).clamp(-5e4, 5e4).to(dtype).to(DEV) for s in (3, 4))
+    positions = (torch.arange(total, dtype=torch.int32) * 5 + 2).to(DEV)
+    table = table.to(DEV)
+    got = []
+    for step in (total, 5000):
+        pages = _pool(n_pages, kv, dim, page)
+        mass = torch.full((n_pages, kv, page), 7.5, device=DEV)
+        pos = torch.full((n_pages, kv, page), -1, dtype=torch.int32, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = [torch.full((total + 3, kv, dim), 9.0, dtype=BF, device=DEV) for _ in range(2)]
+        for lo in range(0, total, step):
+            hi = min(lo + step, total)
+            part = [max(0, min(hi, int(cu[b + 1])) - max(lo, int(cu[b]))) for b in range(len(new))]
+            done = [max(0, min(hi, int(cu[b + 1])) - int(cu[b])) for b in range(len(new))]
+            ln = torch.tensor([a + d for a, d in zip(before, done)], dtype=torch.int32, device=DEV)
+            c = _cu(part).to(DEV)
+            sz.kv4_append(pages, k[lo:hi], v[lo:hi], table, ln, cu=c, positions=positions[lo:hi], mass=mass, pos=pos,
+                          status=status)
+            n = hi - lo + (3 if hi == total else 0)
+            sz.kv4_read(pages, table, ln, dim, cu=c, n_tokens=n, out=[o[lo:lo + n] for o in out])
+        torch.cuda.synchronize()
+        assert int(status.item()) != 0
+        got.append((pages, mass, pos, *out))
+    for one, many in zip(*got):
+        assert torch.equal(one, many)
+    off = int(cu[5])
+    k_out = got[0][3]
+    assert bool((k_out[off + page - 1:off + min(2 * page - 1, 1002)] == 9.0).all())
+    kq = R.quantize(k[:off + page - 1].float())[0]
+    assert torch.equal(k_out[:off + page - 1].double(), kq)
+    hk, _ = sz.kv4_read(got[0][0], table, torch.tensor(lens, dtype=torch.int32, device=DEV), dim, cu=cu.to(DEV),
+                        n_tokens=total, dtype=HF)
+    assert torch.equal(hk[:off + page - 1], kq.to(HF))
+
+
 @pytest.mark.parametrize("dtype", [HF, E5])
 def test_every_pattern_of_the_other_types(dtype):
     """Each FP16 or E5M2 pattern as the first of a block of 2, -1.5, .. times it, and beside ones."""
